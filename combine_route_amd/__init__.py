@@ -825,3 +825,6 @@ class EpDispatchCombineOp:
             self.close()
         except Exception:
             pass
+
+
+from .moe import MOE_EXPORTED, MOE_FP32, moe_rms_norm  # noqa: E402

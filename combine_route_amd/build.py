@@ -12,7 +12,8 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libcombine_route_amd.so")
 SOURCES = [os.path.join(PKG, "csrc", f)
            for f in ("ep_plan.cpp", "ep_kernels.hip", "ep_expert.hip", "ep_wire.hip",
-                     "ep_standard.hip", "ep_probe.hip", "ep_static.hip")]
+                     "ep_standard.hip", "ep_probe.hip", "ep_static.hip", "moe_host.cpp",
+                     "moe_norm.hip")]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1,0 +1,152 @@
+// Host side of include/moe.h: argument checks, launch geometry and launches of
+// the layer operators. As in ep_plan.cpp, every precondition is checked before
+// anything is enqueued and a failed check names the argument.
+#include "moe.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include "ep_static.h"
+#include "moe_kernels.h"
+
+namespace {
+
+constexpr size_t kPtrAlign = 16;
+// Bytes a call may move before its rows stream past the caches: the 256 MB
+// last-level cache of an MI355X.
+constexpr int64_t kKeepBytes = 256ll << 20;
+
+int fail(int code, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return ep::set_error(code, buf);
+}
+
+int ok() { return ep::set_error(EP_OK, ""); }
+
+struct Pointer {
+    const void* ptr;
+    const char* name;
+    size_t align;
+    bool required;
+};
+
+int check_pointers(const Pointer* p, int n)
+{
+    for (int i = 0; i < n; ++i) {
+        if (!p[i].ptr) {
+            if (p[i].required)
+                return fail(EP_ERR_NULL, "%s is NULL", p[i].name);
+            continue;
+        }
+        if (reinterpret_cast<uintptr_t>(p[i].ptr) % p[i].align)
+            return fail(EP_ERR_ALIGN, "%s = %p is not %zu-byte aligned", p[i].name, p[i].ptr,
+                        p[i].align);
+    }
+    return EP_OK;
+}
+
+template <int N>
+int check_pointers(const Pointer (&p)[N])
+{
+    return check_pointers(p, N);
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_rms_norm(const moe_rms_norm_args_t* a, void* stream_ptr)
+{
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    if (a->dtype != EP_BF16 && a->dtype != EP_FP16)
+        return fail(EP_ERR_ARG, "args.dtype = %d: must be EP_BF16 or EP_FP16", a->dtype);
+    if (a->weight_dtype != a->dtype && a->weight_dtype != MOE_FP32)
+        return fail(EP_ERR_ARG, "args.weight_dtype = %d: must be args.dtype or MOE_FP32",
+                    a->weight_dtype);
+    if (a->rows < 0)
+        return fail(EP_ERR_ARG, "args.rows = %lld: must be >= 0", (long long)a->rows);
+    if (a->hidden < 8 || a->hidden % 8)
+        return fail(EP_ERR_ARG, "args.hidden = %d: must be a positive multiple of 8", a->hidden);
+    if (a->hidden > moe::kNormMaxHidden)
+        return fail(EP_ERR_SIZE, "args.hidden = %d: must be at most %d", a->hidden,
+                    moe::kNormMaxHidden);
+    if (!(a->eps >= 0.0f) || std::isinf(a->eps))
+        return fail(EP_ERR_ARG, "args.eps = %g: must be finite and >= 0", (double)a->eps);
+    if ((a->codes == nullptr) != (a->scales == nullptr))
+        return fail(EP_ERR_ARG, "args.codes and args.scales must both be set or both NULL");
+    if (a->codes && a->hidden % 128)
+        return fail(EP_ERR_ARG, "args.hidden = %d: codes need a multiple of 128", a->hidden);
+    if ((a->residual == nullptr) != (a->residual_out == nullptr))
+        return fail(EP_ERR_ARG,
+                    "args.residual and args.residual_out must both be set or both NULL");
+    if (a->row_counts && (a->group_rows < 1 || a->rows % a->group_rows))
+        return fail(EP_ERR_ARG, "args.group_rows = %lld: must be >= 1 and divide rows = %lld",
+                    (long long)a->group_rows, (long long)a->rows);
+    if (a->rows == 0)
+        return ok();
+    if (!a->out && !a->codes)
+        return fail(EP_ERR_NULL, "args.out and args.codes are both NULL");
+    const Pointer ptrs[] = {{a->x, "args.x", kPtrAlign, true},
+                            {a->residual, "args.residual", kPtrAlign, false},
+                            {a->residual_out, "args.residual_out", kPtrAlign, false},
+                            {a->weight, "args.weight", kPtrAlign, true},
+                            {a->out, "args.out", kPtrAlign, false},
+                            {a->codes, "args.codes", kPtrAlign, false},
+                            {a->scales, "args.scales", 4, false},
+                            {a->row_counts, "args.row_counts", 4, false}};
+    const int rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+
+    moe::NormArgs na;
+    na.x = static_cast<const uint8_t*>(a->x);
+    na.res = static_cast<const uint8_t*>(a->residual);
+    na.res_out = static_cast<uint8_t*>(a->residual_out);
+    na.w = static_cast<const uint8_t*>(a->weight);
+    na.out = static_cast<uint8_t*>(a->out);
+    na.codes = static_cast<uint8_t*>(a->codes);
+    na.scales = reinterpret_cast<uint8_t*>(a->scales);
+    na.counts = a->row_counts;
+    na.rows = a->rows;
+    na.group_rows = a->row_counts ? a->group_rows : a->rows;
+    na.H = a->hidden;
+    na.eps = a->eps;
+    // Waves a row: as few as hold it, doubled while the call has fewer waves
+    // than the chip holds at 8 a SIMD and a wave has more than one chunk.
+    const int chunks = (a->hidden + moe::kNormChunk - 1) / moe::kNormChunk;
+    int waves = 1;
+    while (waves * moe::kNormChunks < chunks)
+        waves *= 2;
+    while (waves < moe::kNormMaxWaves && waves < chunks && a->rows * waves < 8192)
+        waves *= 2;
+    na.row_waves = waves;
+    na.chunks = (chunks + waves - 1) / waves;
+    // a launch's work-items must fit in 32 bits
+    if (a->rows > ((int64_t)UINT32_MAX - 1024) / (waves * ep::kWave))
+        return fail(EP_ERR_SIZE, "args.rows = %lld is too large for one launch",
+                    (long long)a->rows);
+    const int64_t row_bytes = (int64_t)a->hidden *
+                              (2 + (a->residual ? 4 : 0) + (a->out ? 2 : 0) + (a->codes ? 1 : 0));
+    const bool streaming = a->rows * row_bytes > kKeepBytes;
+    const hipError_t e = moe::launch_norm(na, a->dtype == EP_BF16 ? 0 : 1,
+                                          a->weight_dtype == MOE_FP32 ? 2
+                                          : a->dtype == EP_BF16       ? 0
+                                                                      : 1,
+                                          streaming, static_cast<hipStream_t>(stream_ptr));
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "rms_norm launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+}  // extern "C"

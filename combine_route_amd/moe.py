@@ -1,0 +1,116 @@
+"""Python binding of include/moe.h: the layer operators around the dispatch
+and the combine. As the rest of the package it only marshals arguments: every
+tensor is checked to be a contiguous device tensor of the right element type
+and shape, all on one device, before a pointer reaches the library, and the
+call runs on that device, on the given stream or torch's current one there.
+"""
+import contextlib
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import (_F32, _I32, EP_BF16, EP_FP16, EpError, _check, _dev, _stream, load)
+
+MOE_FP32 = 3
+MOE_EXPORTED = ("moe_rms_norm",)
+
+_DTYPE_CODE = {torch.bfloat16: EP_BF16, torch.float16: EP_FP16}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+class MoeRmsNormArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "x", "residual", "residual_out", "weight", "out", "codes", "scales", "row_counts")] +
+        [("rows", ctypes.c_int64), ("group_rows", ctypes.c_int64), ("hidden", ctypes.c_int32),
+         ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float)])
+
+
+def _declare(lib):
+    """Argument types of the moe_ functions, once a library."""
+    if getattr(lib, "_moe_declared", False):
+        return lib
+    V = ctypes.c_void_p
+    lib.moe_rms_norm.argtypes = [ctypes.POINTER(MoeRmsNormArgs), V]
+    for name in MOE_EXPORTED:
+        getattr(lib, name).restype = ctypes.c_int
+    lib._moe_declared = True
+    return lib
+
+
+def _lib():
+    return _declare(load())
+
+
+def _shaped(t: Optional[torch.Tensor], name: str, shape, dtypes):
+    """Address of a tensor that has exactly this shape; None stays None."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    nbytes = t.numel() * t.element_size() if isinstance(t, torch.Tensor) else 0
+    return _dev(t, name, nbytes, dtypes)
+
+
+def _device_of(**tensors) -> int:
+    """The one device all of a call's tensors are on."""
+    index = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on the GPU, not {t.device}")
+        if index is None:
+            index = t.device.index
+        elif t.device.index != index:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
+    return index
+
+
+def _call(fn, index, stream, *args):
+    """One library call with `index` the current device."""
+    other = torch.cuda.current_device() != index
+    with torch.cuda.device(index) if other else contextlib.nullcontext():
+        _check(fn, getattr(_lib(), fn)(*args, _stream(stream, index)))
+
+
+def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                 out: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None,
+                 codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                 counts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_rms_norm() (include/moe.h): RMS norm of x's rows [..., H] (bf16 or
+    fp16) times weight [H] (x's type or float32), after the residual's
+    addition. residual_out (default: residual, in place) gets x + residual;
+    out the normed rows in x's type; codes [..., H] and scales [..., H / 128]
+    the same rows as E4M3 with a scale per 128 elements. counts: an int32
+    tensor of one count per leading index of x ([G, R, H] rows with counts
+    [G]); only the first counts[g] rows of group g are read and written."""
+    index = _device_of(x=x, weight=weight, out=out, residual=residual, residual_out=residual_out,
+                       codes=codes, scales=scales, counts=counts)
+    dtype = _DTYPE_CODE.get(x.dtype)
+    if dtype is None:
+        raise ValueError(f"x must be bf16 or fp16, not {x.dtype}")
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x must have rows of at least one element")
+    H = x.shape[-1]
+    rows = x.numel() // H
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    same = (x.dtype,)
+    group = 0
+    if counts is not None:
+        if x.dim() < 2 or x.shape[0] == 0:
+            raise ValueError("counts needs rows of shape [G, ..., H] with G >= 1")
+        group = max(1, rows // x.shape[0])
+    a = MoeRmsNormArgs(
+        _shaped(x, "x", x.shape, same), _shaped(residual, "residual", x.shape, same),
+        _shaped(residual_out, "residual_out", x.shape, same),
+        _shaped(weight, "weight", (H,), (x.dtype, torch.float32)),
+        _shaped(out, "out", x.shape, same), _shaped(codes, "codes", x.shape, _CODES),
+        _shaped(scales, "scales", x.shape[:-1] + (H // 128,), _F32),
+        _shaped(counts, "counts", x.shape[:1], _I32), rows, group, H, dtype,
+        MOE_FP32 if weight.dtype == torch.float32 else dtype, eps)
+    _call("moe_rms_norm", index, stream, ctypes.byref(a))

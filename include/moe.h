@@ -1,0 +1,90 @@
+/*
+ * combine_route_amd: the layer around the dispatch and the combine.
+ *
+ * Operators that make the rows a dispatch sends, read the expert-major rows
+ * it leaves, and take the gradient of the two fused calls. They live in the
+ * same library as ep.h's functions (libcombine_route_amd.so) and share its
+ * types, error codes, ep_last_error() and conventions:
+ *  - Every call returns EP_OK or a negative EP_ERR_* code; every precondition
+ *    that sizes and pointers allow is checked on the host before anything is
+ *    enqueued, and on error nothing is enqueued and no output is touched.
+ *  - Calls are asynchronous on stream (a hipStream_t; NULL = the default
+ *    stream), allocate nothing, do not synchronise and can be captured in a
+ *    HIP graph. Every buffer and the stream belong to the current device.
+ *  - Buffers are caller-owned, contiguous device memory and must not overlap
+ *    unless an argument says so.
+ *  - Results are deterministic bit for bit: no atomic decides an order.
+ *    They do not depend on what a buffer held before or on launch geometry.
+ *  - The two calls without a plan (moe_rms_norm, moe_grouped_gemm) keep no
+ *    state: any number of threads and streams may call them at once.
+ *  - ep_plan_set_timing does not cover these calls.
+ *
+ * Block scales follow EP_WIRE_FP8_BLOCK128: value = E4M3 code * scale, one
+ * FP32 scale per 128 consecutive elements of a row. Rows written here are
+ * quantized as follows (amax: the block's largest magnitude, u = max(amax,
+ * 2^-100)): scale = u / 448, code = E4M3(v * (448 / u)) to nearest even,
+ * saturating at +-448; an all-zero block gets scale 1. (ep_quantize_rows does
+ * the same for blocks whose amax is at least 2^-100.) A NaN element gets the
+ * NaN code 0x7F; a block holding an infinity gets an infinite scale.
+ */
+#ifndef COMBINE_ROUTE_AMD_MOE_H
+#define COMBINE_ROUTE_AMD_MOE_H
+
+#include "ep.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* A weight type beside EP_BF16 and EP_FP16 (moe_rms_norm's weight). */
+enum { MOE_FP32 = 3 };
+
+/* RMS norm of rows, with the residual's addition, into rows of the same type
+ * and / or FP8 rows with block scales (the payload and scales an FP8 dispatch
+ * with scale_dim = hidden / 128 sends).
+ *   x             [rows][hidden] of dtype (EP_BF16 or EP_FP16).
+ *   residual      [rows][hidden] of dtype, or NULL. Given, h = x + residual in
+ *                 FP32, rounded to nearest even to dtype; else h = x.
+ *   residual_out  [rows][hidden]: h, NULL iff residual is NULL. May be the
+ *                 residual itself (in place).
+ *   weight        [hidden] of weight_dtype (dtype itself, or MOE_FP32).
+ *   out           [rows][hidden] of dtype, or NULL: y = h * r * weight with r
+ *                 = 1 / sqrt(mean(h^2) + eps), all in FP32, rounded once.
+ *                 May be x itself (in place).
+ *   codes, scales [rows][hidden] E4M3 and [rows][hidden / 128] float, or both
+ *                 NULL: y (the FP32 value, not the rounded out) quantized.
+ *                 Need hidden % 128 == 0.
+ *   row_counts, group_rows  as ep_quantize_rows: NULL for every row, or a
+ *                 device int32 [rows / group_rows] array; in group g only the
+ *                 first row_counts[g] rows are read and written (a count
+ *                 above group_rows means all of them, one below 0 none).
+ * One of out and codes is required. hidden: a multiple of 8, 8 to 65536;
+ * x, residual, residual_out, out, codes and weight 16-byte aligned, scales
+ * and row_counts 4-byte. eps >= 0 and finite.
+ * Errors: EP_ERR_NULL, EP_ERR_ALIGN, EP_ERR_ARG, EP_ERR_SIZE (hidden above
+ * 65536, or rows whose waves, one per up to 4096 elements, exceed 2^26),
+ * EP_ERR_HIP. rows == 0 returns EP_OK whatever the pointers are. */
+typedef struct moe_rms_norm_args {
+    const void *x;
+    const void *residual;
+    void *residual_out;
+    const void *weight;
+    void *out;
+    void *codes;
+    float *scales;
+    const int32_t *row_counts;
+    int64_t rows;
+    int64_t group_rows;
+    int32_t hidden;
+    int32_t dtype;
+    int32_t weight_dtype;
+    float eps;
+} moe_rms_norm_args_t;
+
+int moe_rms_norm(const moe_rms_norm_args_t *args, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* COMBINE_ROUTE_AMD_MOE_H */

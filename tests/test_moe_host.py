@@ -1,0 +1,95 @@
+"""Host-side checks of include/moe.h (no GPU needed, no kernel is launched):
+every function is exported, and every bad argument is refused with its code
+and a message that names it, before anything is enqueued. Pointers are fake
+addresses that are never dereferenced."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+
+import combine_route_amd as cra
+from combine_route_amd import moe
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x7F1000000000             # 16-byte aligned device-looking address
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(cra.LIB_PATH):
+        import combine_route_amd.build as b
+        b.build()
+    return moe._lib()
+
+
+def test_exports_every_declared_function(lib):
+    with open(os.path.join(ROOT, "include", "moe.h")) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    names = set(re.findall(r"\b(moe_[a-z_]+)\s*\(", text))
+    assert sorted(names) == sorted(moe.MOE_EXPORTED)
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def norm_args(**kw):
+    a = dict(x=FAKE, residual=FAKE, residual_out=FAKE, weight=FAKE, out=FAKE, codes=FAKE,
+             scales=FAKE, row_counts=FAKE, rows=64, group_rows=16, hidden=256, dtype=cra.EP_BF16,
+             weight_dtype=cra.EP_BF16, eps=1e-6)
+    a.update(kw)
+    return moe.MoeRmsNormArgs(**a)
+
+
+BAD_NORM = [
+    (dict(x=None), cra.EP_ERR_NULL, "x"),
+    (dict(weight=None), cra.EP_ERR_NULL, "weight"),
+    (dict(out=None, codes=None, scales=None), cra.EP_ERR_NULL, "out"),
+    (dict(codes=None), cra.EP_ERR_ARG, "scales"),
+    (dict(scales=None), cra.EP_ERR_ARG, "codes"),
+    (dict(residual=None), cra.EP_ERR_ARG, "residual"),
+    (dict(residual_out=None), cra.EP_ERR_ARG, "residual_out"),
+    (dict(x=FAKE + 8), cra.EP_ERR_ALIGN, "x"),
+    (dict(residual=FAKE + 2), cra.EP_ERR_ALIGN, "residual"),
+    (dict(residual_out=FAKE + 2), cra.EP_ERR_ALIGN, "residual_out"),
+    (dict(weight=FAKE + 4), cra.EP_ERR_ALIGN, "weight"),
+    (dict(out=FAKE + 8), cra.EP_ERR_ALIGN, "out"),
+    (dict(codes=FAKE + 8), cra.EP_ERR_ALIGN, "codes"),
+    (dict(scales=FAKE + 2), cra.EP_ERR_ALIGN, "scales"),
+    (dict(row_counts=FAKE + 2), cra.EP_ERR_ALIGN, "row_counts"),
+    (dict(rows=-1), cra.EP_ERR_ARG, "rows"),
+    (dict(group_rows=0), cra.EP_ERR_ARG, "group_rows"),
+    (dict(group_rows=7), cra.EP_ERR_ARG, "group_rows"),
+    (dict(hidden=0), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=-8), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=12), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=136), cra.EP_ERR_ARG, "multiple of 128"),
+    (dict(hidden=65536 + 128), cra.EP_ERR_SIZE, "hidden"),
+    (dict(dtype=cra.EP_FP8_E4M3), cra.EP_ERR_ARG, "dtype"),
+    (dict(weight_dtype=cra.EP_FP16), cra.EP_ERR_ARG, "weight_dtype"),
+    (dict(eps=-1.0), cra.EP_ERR_ARG, "eps"),
+    (dict(eps=math.nan), cra.EP_ERR_ARG, "eps"),
+    (dict(eps=math.inf), cra.EP_ERR_ARG, "eps"),
+    (dict(rows=1 << 27, group_rows=1 << 20), cra.EP_ERR_SIZE, "rows"),
+]
+
+
+@pytest.mark.parametrize("change,code,word", BAD_NORM)
+def test_rms_norm_refuses(lib, change, code, word):
+    assert lib.moe_rms_norm(ctypes.byref(norm_args(**change)), None) == code
+    assert word in cra.ep_last_error()
+
+
+def test_rms_norm_without_rows_is_no_work(lib):
+    assert lib.moe_rms_norm(None, None) == cra.EP_ERR_NULL
+    assert lib.moe_rms_norm(ctypes.byref(norm_args(rows=0, x=None, out=None)), None) == cra.EP_OK
+    assert cra.ep_last_error() == ""
+
+
+def test_tensors_off_the_gpu_are_refused():
+    import torch
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        cra.moe_rms_norm(x, torch.ones(128, dtype=torch.bfloat16), 1e-6, out=x)
+    with pytest.raises(TypeError, match="weight"):
+        moe._device_of(weight=[1.0])
