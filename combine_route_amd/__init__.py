@@ -811,6 +811,55 @@ class EpDispatchCombineOp:
             ex["plan"], ctypes.byref(c[1]), _stream(stream, self._dev_index)))
         return self.combine_out
 
+    def combine_standard_moe_backward(self, grad_out, weights, indices, packed_y=None,
+                                      grad_packed_y=None, grad_weights=None, stream=None):
+        """Gradient of combine_standard_moe for the last dispatch_standard_moe:
+        grad_out [W, M, H] of its result; weights, indices and packed_y its
+        weights, ids and input. Returns (grad_packed_y [W, Er, cap, H],
+        grad_weights [W, M, k]); the second is None without packed_y, and only
+        taken with weights. Rows of no kept pair and of tokens t >= T_r are
+        left untouched. The results are the tensors given for them, or new
+        ones (zeros)."""
+        ex = self._fused_state("combine_standard_moe_backward")
+        cfg = self.cfg
+        W, M, k = cfg.world_size, cfg.max_num_inp_token_per_rank, cfg.num_experts_per_token
+        if grad_packed_y is None:
+            grad_packed_y = self._zeros((W, cfg.num_experts_per_rank, self.expert_capacity,
+                                         cfg.hidden_dim), _TORCH[cfg.combine_dtype], stream)
+        if grad_weights is None and packed_y is not None:
+            grad_weights = self._zeros((W, M, k), torch.float32, stream)
+        moe_combine_backward(ex["plan"], cfg, self.expert_capacity, grad_out, indices, weights,
+                             packed_y, grad_packed_y, grad_weights, stream)
+        return grad_packed_y, grad_weights
+
+    def dispatch_standard_moe_backward(self, grad_packed_x, grad_x=None, stream=None):
+        """Gradient of dispatch_standard_moe's rows: grad_x [W, M, H] from
+        grad_packed_x [W, Er, cap, H], both in the combine type. Rows of
+        tokens t >= T_r are left untouched. Returns the tensor given for it,
+        or a new one (zeros)."""
+        ex = self._fused_state("dispatch_standard_moe_backward")
+        cfg = self.cfg
+        if grad_x is None:
+            grad_x = self._zeros((cfg.world_size, cfg.max_num_inp_token_per_rank, cfg.hidden_dim),
+                                 _TORCH[cfg.combine_dtype], stream)
+        moe_dispatch_backward(ex["plan"], cfg, self.expert_capacity, grad_packed_x, grad_x, stream)
+        return grad_x
+
+    def _zeros(self, shape, dtype, stream):
+        """New zeros, filled (and owned by torch's allocator) on the stream
+        the call runs on."""
+        if stream is None:
+            return torch.zeros(shape, dtype=dtype, device=self.workspace.device)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.workspace.device)
+        with torch.cuda.stream(stream):
+            return torch.zeros(shape, dtype=dtype, device=self.workspace.device)
+
+    def _fused_state(self, call):
+        if self._ex is None:
+            raise EpError(call, EP_ERR_STATE, f"{call} before any dispatch_standard_moe")
+        return self._ex
+
     def close(self):
         self._dcache = self._ccache = None
         if self._ex is not None:
@@ -827,4 +876,5 @@ class EpDispatchCombineOp:
             pass
 
 
-from .moe import MOE_EXPORTED, MOE_FP32, moe_rms_norm  # noqa: E402
+from .moe import (MOE_EXPORTED, MOE_FP32, moe_combine_backward, moe_dispatch_backward,  # noqa: E402
+                  moe_rms_norm)

@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "ep_kernels.h"
+#include "ep_plan_view.h"
 #include "ep_static.h"
 
 namespace {
@@ -1614,6 +1615,35 @@ int ep_plan_kernel_time(ep_plan_t* p, int kernel, int32_t* count, double* total_
 namespace ep {
 
 int set_error(int code, const char* msg) { return fail(code, "%s", msg); }
+
+int fused_view(const ep_expert_plan_t* x, const char* call, FusedView* v)
+{
+    if (!x)
+        return fail(EP_ERR_NULL, "plan is NULL");
+    if (!x->fused)
+        return fail(EP_ERR_STATE, "%s before any dispatch_standard_moe on this expert plan (or a "
+                    "convert_dispatch_output came since)", call);
+    const ep_plan* p = x->plan;
+    v->M = p->s.M;
+    v->k = p->s.k;
+    v->Er = p->s.Er;
+    v->E = (int32_t)p->s.E;
+    v->H = p->s.H;
+    v->cap = x->e.cap;
+    v->dtype = p->cfg.combine_dtype;
+    v->wire = p->cfg.combine_wire;
+    v->fslot = reinterpret_cast<const int32_t*>(x->ws + x->e.off_efwd);
+    token_map(p->s, x->fused_ntok, &v->tokens);
+    v->large = large_call(p->s, x->fused_ntok);
+    v->stream = effective_launch(p, x->fused_ntok).expert_cache_policy == EP_CACHE_STREAM;
+    return EP_OK;
+}
+
+void fused_launched(ep_expert_plan_t* x, hipStream_t stream)
+{
+    x->launched = true;
+    x->last_stream = stream;
+}
 
 // The per-device plans of ep_plan_static, over the library's static scratch.
 ep_plan g_static_plans[kMaxDevices];

@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdio>
 
+#include "ep_plan_view.h"
 #include "ep_static.h"
 #include "moe_kernels.h"
 
@@ -146,6 +147,105 @@ int moe_rms_norm(const moe_rms_norm_args_t* a, void* stream_ptr)
                                           streaming, static_cast<hipStream_t>(stream_ptr));
     if (e != hipSuccess)
         return fail(EP_ERR_HIP, "rms_norm launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int moe_combine_backward(ep_expert_plan_t* x, const moe_combine_backward_args_t* a,
+                         void* stream_ptr)
+{
+    if (!x)
+        return fail(EP_ERR_NULL, "plan is NULL");
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    const Pointer ptrs[] = {{a->grad_out, "args.grad_out", kPtrAlign, true},
+                            {a->indices, "args.indices", 4, true},
+                            {a->weights, "args.weights", 4, false},
+                            {a->packed_y, "args.packed_y", kPtrAlign, false},
+                            {a->grad_packed_y, "args.grad_packed_y", kPtrAlign, true},
+                            {a->grad_weights, "args.grad_weights", 4, false}};
+    int rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+    if ((a->packed_y == nullptr) != (a->grad_weights == nullptr))
+        return fail(EP_ERR_ARG,
+                    "args.packed_y and args.grad_weights must both be set or both NULL");
+    if (a->grad_weights && !a->weights)
+        return fail(EP_ERR_ARG, "args.grad_weights needs args.weights");
+    ep::FusedView v;
+    rc = ep::fused_view(x, "combine_backward", &v);
+    if (rc != EP_OK)
+        return rc;
+    if (v.wire != EP_WIRE_NONE)
+        return fail(EP_ERR_ARG, "combine_backward needs cfg.combine_wire = EP_WIRE_NONE");
+    moe::CombineBackwardArgs ca;
+    ca.go = static_cast<const uint8_t*>(a->grad_out);
+    ca.idx = a->indices;
+    ca.w = a->weights;
+    ca.py = static_cast<const uint8_t*>(a->packed_y);
+    ca.fslot = v.fslot;
+    ca.gy = static_cast<uint8_t*>(a->grad_packed_y);
+    ca.gw = a->grad_weights;
+    ca.row_vecs = v.H / 8;
+    ca.M = v.M;
+    ca.k = v.k;
+    ca.E = v.E;
+    // Waves a token from the row's length alone (the dots' order depends on
+    // it): as many as give each at most kBackChunks chunks.
+    const int chunks = (v.H + 511) / 512;
+    int waves = 1;
+    while (waves < moe::kBackMaxWaves && waves * moe::kBackChunks < chunks)
+        waves *= 2;
+    ca.row_waves = waves;
+    ca.wave_vecs = (ca.row_vecs + waves - 1) / waves;
+    if (((int64_t)v.tokens.total + 4) * std::max(waves, 4) * ep::kWave > (int64_t)UINT32_MAX)
+        return fail(EP_ERR_SIZE, "combine_backward of %d tokens is too large for one launch",
+                    v.tokens.total);
+    hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+    const hipError_t e = moe::launch_combine_backward(ca, v.tokens, v.dtype == EP_BF16 ? 0 : 1,
+                                                      v.stream, stream);
+    ep::fused_launched(x, stream);
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "combine_backward launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int moe_dispatch_backward(ep_expert_plan_t* x, const moe_dispatch_backward_args_t* a,
+                          void* stream_ptr)
+{
+    if (!x)
+        return fail(EP_ERR_NULL, "plan is NULL");
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    const Pointer ptrs[] = {{a->grad_packed_x, "args.grad_packed_x", kPtrAlign, true},
+                            {a->grad_x, "args.grad_x", kPtrAlign, true}};
+    int rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+    ep::FusedView v;
+    rc = ep::fused_view(x, "dispatch_backward", &v);
+    if (rc != EP_OK)
+        return rc;
+    if (v.wire != EP_WIRE_NONE)
+        return fail(EP_ERR_ARG, "dispatch_backward needs cfg.combine_wire = EP_WIRE_NONE");
+    moe::DispatchBackwardArgs da;
+    da.gp = static_cast<const uint8_t*>(a->grad_packed_x);
+    da.fslot = v.fslot;
+    da.gx = static_cast<uint8_t*>(a->grad_x);
+    da.row_vecs = v.H / 8;
+    da.piece_vecs = ep::kWave;
+    da.pieces = (da.row_vecs + da.piece_vecs - 1) / da.piece_vecs;
+    da.M = v.M;
+    da.k = v.k;
+    const int waves = v.large ? 16 : 4;
+    if (((int64_t)v.tokens.total * da.pieces + waves) * ep::kWave > (int64_t)UINT32_MAX)
+        return fail(EP_ERR_SIZE, "dispatch_backward of %d tokens is too large for one launch",
+                    v.tokens.total);
+    hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+    const hipError_t e = moe::launch_dispatch_backward(da, v.tokens, v.dtype == EP_BF16 ? 0 : 1,
+                                                       waves, v.stream, stream);
+    ep::fused_launched(x, stream);
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "dispatch_backward launch failed: %s", hipGetErrorString(e));
     return ok();
 }
 

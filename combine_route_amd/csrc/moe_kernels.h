@@ -40,4 +40,38 @@ struct NormArgs {
 // dtype, wtype: 0 bf16, 1 fp16 (wtype also 2: fp32).
 hipError_t launch_norm(const NormArgs& a, int dtype, int wtype, bool stream, hipStream_t s);
 
+// moe_backward.hip: gradients of the fused dispatch and combine, through the
+// per-slot map of the expert plan's last fused dispatch.
+constexpr int kBackChunks = 4;       // 512-element chunks a wave holds at a time
+constexpr int kBackMaxWaves = 16;
+
+struct CombineBackwardArgs {
+    const uint8_t* go;           // [W][M][H] gradient of the combined rows
+    const int32_t* idx;          // [W][M][k]
+    const float* w;              // [W][M][k] or null
+    const uint8_t* py;           // [W * Er][cap][H], null without grad_w
+    const int32_t* fslot;        // [W][M][k]
+    uint8_t* gy;                 // [W * Er][cap][H]
+    float* gw;                   // [W][M][k] or null
+    int32_t row_vecs;            // 16-byte vectors a row
+    int32_t row_waves;           // waves a token: a power of two up to kBackMaxWaves
+    int32_t wave_vecs;           // vectors of a wave's share of the row
+    int32_t M, k, E;
+};
+
+struct DispatchBackwardArgs {
+    const uint8_t* gp;           // [W * Er][cap][H] gradient of the packed rows
+    const int32_t* fslot;        // [W][M][k]
+    uint8_t* gx;                 // [W][M][H]
+    int32_t row_vecs;
+    int32_t piece_vecs;          // vectors a wave sums: 64 or 128
+    int32_t pieces;
+    int32_t M, k;
+};
+
+hipError_t launch_combine_backward(const CombineBackwardArgs& a, const ep::TokenMap& tk, int dtype,
+                                   bool stream, hipStream_t s);
+hipError_t launch_dispatch_backward(const DispatchBackwardArgs& a, const ep::TokenMap& tk,
+                                    int dtype, int waves, bool stream, hipStream_t s);
+
 }  // namespace moe

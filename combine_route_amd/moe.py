@@ -10,10 +10,11 @@ from typing import Optional
 
 import torch
 
-from . import (_F32, _I32, EP_BF16, EP_FP16, EpError, _check, _dev, _stream, load)
+from . import (_F32, _I32, _TORCH, EP_BF16, EP_FP16, EpConfig, _check, _dev, _sizes, _stream,
+               load)
 
 MOE_FP32 = 3
-MOE_EXPORTED = ("moe_rms_norm",)
+MOE_EXPORTED = ("moe_rms_norm", "moe_combine_backward", "moe_dispatch_backward")
 
 _DTYPE_CODE = {torch.bfloat16: EP_BF16, torch.float16: EP_FP16}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -26,12 +27,23 @@ class MoeRmsNormArgs(ctypes.Structure):
          ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float)])
 
 
+class MoeCombineBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "grad_out", "indices", "weights", "packed_y", "grad_packed_y", "grad_weights")]
+
+
+class MoeDispatchBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("grad_packed_x", "grad_x")]
+
+
 def _declare(lib):
     """Argument types of the moe_ functions, once a library."""
     if getattr(lib, "_moe_declared", False):
         return lib
     V = ctypes.c_void_p
     lib.moe_rms_norm.argtypes = [ctypes.POINTER(MoeRmsNormArgs), V]
+    lib.moe_combine_backward.argtypes = [V, ctypes.POINTER(MoeCombineBackwardArgs), V]
+    lib.moe_dispatch_backward.argtypes = [V, ctypes.POINTER(MoeDispatchBackwardArgs), V]
     for name in MOE_EXPORTED:
         getattr(lib, name).restype = ctypes.c_int
     lib._moe_declared = True
@@ -114,3 +126,35 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
         _shaped(counts, "counts", x.shape[:1], _I32), rows, group, H, dtype,
         MOE_FP32 if weight.dtype == torch.float32 else dtype, eps)
     _call("moe_rms_norm", index, stream, ctypes.byref(a))
+
+
+def _packed_shape(cfg: EpConfig, cap: int):
+    return (cfg.world_size, cfg.num_experts_per_rank, cap, cfg.hidden_dim)
+
+
+def moe_combine_backward(eplan: int, cfg: EpConfig, cap: int, grad_out, indices, weights, packed_y,
+                         grad_packed_y, grad_weights, stream=None) -> None:
+    """moe_combine_backward(); tensors as in include/moe.h."""
+    index = _device_of(grad_out=grad_out, indices=indices, weights=weights, packed_y=packed_y,
+                       grad_packed_y=grad_packed_y, grad_weights=grad_weights)
+    W, M, k, _, _, _ = _sizes(cfg)
+    rows, slots = (W, M, cfg.hidden_dim), (W, M, k)
+    packed, dt = _packed_shape(cfg, cap), (_TORCH[cfg.combine_dtype],)
+    a = MoeCombineBackwardArgs(
+        _shaped(grad_out, "grad_out", rows, dt), _shaped(indices, "indices", slots, _I32),
+        _shaped(weights, "weights", slots, _F32), _shaped(packed_y, "packed_y", packed, dt),
+        _shaped(grad_packed_y, "grad_packed_y", packed, dt),
+        _shaped(grad_weights, "grad_weights", slots, _F32))
+    _call("moe_combine_backward", index, stream, eplan, ctypes.byref(a))
+
+
+def moe_dispatch_backward(eplan: int, cfg: EpConfig, cap: int, grad_packed_x, grad_x,
+                          stream=None) -> None:
+    """moe_dispatch_backward(); tensors as in include/moe.h."""
+    index = _device_of(grad_packed_x=grad_packed_x, grad_x=grad_x)
+    W, M, _, _, _, _ = _sizes(cfg)
+    dt = (_TORCH[cfg.combine_dtype],)
+    a = MoeDispatchBackwardArgs(
+        _shaped(grad_packed_x, "grad_packed_x", _packed_shape(cfg, cap), dt),
+        _shaped(grad_x, "grad_x", (W, M, cfg.hidden_dim), dt))
+    _call("moe_dispatch_backward", index, stream, eplan, ctypes.byref(a))

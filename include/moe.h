@@ -83,6 +83,65 @@ typedef struct moe_rms_norm_args {
 
 int moe_rms_norm(const moe_rms_norm_args_t *args, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Gradients of the fused calls. Both use the map of the last
+ * ep_dispatch_standard_moe on the expert plan, as ep_combine_standard_moe
+ * does (a later ep_convert_dispatch_output on the plan ends it); they may be
+ * called any number of times per dispatch. Gradients are taken through the
+ * calls' sums in FP32: the combine's rounding of each rank's part and of the
+ * result count as the identity, and so does a dispatch_cast. W, M, k, Er, H
+ * and cap are the plan's, rows have its combine_dtype (whatever its
+ * dispatch_dtype), and its combine_wire must be EP_WIRE_NONE.
+ * ------------------------------------------------------------------------ */
+
+/* Gradient of ep_combine_standard_moe.
+ *   grad_out       [W][M][H]: of out; rows t < T_r are read.
+ *   indices        [W][M][k]: the ids of the dispatch.
+ *   weights        [W][M][k] float the combine applied, or NULL (plain sum).
+ *   packed_y       [W][Er][cap][H] the combine's input; NULL iff grad_weights
+ *                  is NULL.
+ *   grad_packed_y  [W][Er][cap][H]: for each kept (token, expert) pair c *
+ *                  grad_out's row, one FP32 product rounded once, c the FP32
+ *                  sum in slot order of the weights on the slots naming the
+ *                  expert (1 without weights). Slots past min(count, cap)
+ *                  are left untouched.
+ *   grad_weights   [W][M][k] float, or NULL: for each slot of tokens t < T_r
+ *                  the FP32 dot product of grad_out's row and the kept row of
+ *                  packed_y of the slot's expert (slots naming one expert get
+ *                  the same value); 0 for a slot whose pair was dropped or
+ *                  whose id names no expert. Rows t >= T_r are left
+ *                  untouched. Needs weights.
+ * Rows 16-byte aligned, indices and weights 4-byte.
+ * Errors: EP_ERR_NULL, EP_ERR_ALIGN, EP_ERR_ARG (pairings, a combine_wire),
+ * EP_ERR_STATE (no fused dispatch), EP_ERR_SIZE (too many work-items for a
+ * launch), EP_ERR_HIP. */
+typedef struct moe_combine_backward_args {
+    const void *grad_out;
+    const int32_t *indices;
+    const float *weights;
+    const void *packed_y;
+    void *grad_packed_y;
+    float *grad_weights;
+} moe_combine_backward_args_t;
+
+int moe_combine_backward(ep_expert_plan_t *plan, const moe_combine_backward_args_t *args,
+                         void *stream);
+
+/* Gradient of ep_dispatch_standard_moe's rows.
+ *   grad_packed_x  [W][Er][cap][H] (slots past min(count, cap) are not read).
+ *   grad_x         [W][M][H]: for each token t < T_r the FP32 sum in slot
+ *                  order, from the first, of its kept pairs' rows, rounded to
+ *                  nearest even once; +0 for a token with none. Rows t >= T_r
+ *                  are left untouched.
+ * 16-byte aligned. Errors as moe_combine_backward. */
+typedef struct moe_dispatch_backward_args {
+    const void *grad_packed_x;
+    void *grad_x;
+} moe_dispatch_backward_args_t;
+
+int moe_dispatch_backward(ep_expert_plan_t *plan, const moe_dispatch_backward_args_t *args,
+                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -65,3 +65,27 @@ def rms_norm(x, weight, eps, residual=None):
         h = (x.float() + residual.float()).to(x.dtype).double()
     ms = (h * h).mean(-1, keepdim=True)
     return h, h / torch.sqrt(ms + eps) * weight.double()
+
+
+def packed_rows(ids, ntok, E, cap):
+    """ids [W, M, k] on the CPU -> ([W, M, k] packed row e * cap + p of each
+    slot that is its expert's first in the token and within the capacity, else
+    -1; [W, M, k] the first slot naming the slot's expert, -1 for none). An
+    expert's rows are in source rank, then token order."""
+    W, M, k = ids.shape
+    rows = torch.full(ids.shape, -1, dtype=torch.int64)
+    lead = torch.full(ids.shape, -1, dtype=torch.int64)
+    count = [0] * E
+    for r in range(W):
+        for t in range(ntok[r]):
+            seen = {}
+            for j, e in enumerate(ids[r, t].tolist()):
+                if not 0 <= e < E:
+                    continue
+                if e not in seen:
+                    seen[e] = j
+                    if count[e] < cap:
+                        rows[r, t, j] = e * cap + count[e]
+                    count[e] += 1
+                lead[r, t, j] = seen[e]
+    return rows, lead

@@ -93,3 +93,43 @@ def test_tensors_off_the_gpu_are_refused():
         cra.moe_rms_norm(x, torch.ones(128, dtype=torch.bfloat16), 1e-6, out=x)
     with pytest.raises(TypeError, match="weight"):
         moe._device_of(weight=[1.0])
+
+
+def test_backward_calls_refuse(lib):
+    cb, db = moe.MoeCombineBackwardArgs(*[FAKE] * 6), moe.MoeDispatchBackwardArgs(FAKE, FAKE)
+    assert lib.moe_combine_backward(None, ctypes.byref(cb), None) == cra.EP_ERR_NULL
+    assert lib.moe_dispatch_backward(None, ctypes.byref(db), None) == cra.EP_ERR_NULL
+    cfg = cra.make_config(2, 256, 16, 4, 2)
+    plan, eplan = ctypes.c_void_p(), ctypes.c_void_p()
+    assert lib.ep_plan_create(ctypes.byref(cfg), FAKE, 1 << 40, ctypes.byref(plan)) == 0
+    assert lib.ep_expert_plan_create(plan, 8, FAKE, 1 << 40, ctypes.byref(eplan)) == 0
+
+    def combine(code, word, **change):
+        a = dict(zip([n for n, _ in moe.MoeCombineBackwardArgs._fields_], [FAKE] * 6))
+        a.update(change)
+        args = moe.MoeCombineBackwardArgs(**a)
+        assert lib.moe_combine_backward(eplan, ctypes.byref(args), None) == code
+        assert word in cra.ep_last_error()
+
+    assert lib.moe_combine_backward(eplan, None, None) == cra.EP_ERR_NULL
+    for name in ("grad_out", "indices", "grad_packed_y"):
+        combine(cra.EP_ERR_NULL, name, **{name: None})
+    for name in ("grad_out", "packed_y", "grad_packed_y"):
+        combine(cra.EP_ERR_ALIGN, name, **{name: FAKE + 8})
+    for name in ("indices", "weights", "grad_weights"):
+        combine(cra.EP_ERR_ALIGN, name, **{name: FAKE + 2})
+    combine(cra.EP_ERR_ARG, "packed_y", packed_y=None)
+    combine(cra.EP_ERR_ARG, "packed_y", grad_weights=None)
+    combine(cra.EP_ERR_ARG, "args.weights", weights=None)
+    combine(cra.EP_ERR_STATE, "before any")
+    assert lib.moe_dispatch_backward(eplan, None, None) == cra.EP_ERR_NULL
+    for i, name in enumerate(("grad_packed_x", "grad_x")):
+        for value, code in ((None, cra.EP_ERR_NULL), (FAKE + 8, cra.EP_ERR_ALIGN)):
+            p = [FAKE, FAKE]
+            p[i] = value
+            args = moe.MoeDispatchBackwardArgs(*p)
+            assert lib.moe_dispatch_backward(eplan, ctypes.byref(args), None) == code
+            assert name in cra.ep_last_error()
+    assert lib.moe_dispatch_backward(eplan, ctypes.byref(db), None) == cra.EP_ERR_STATE
+    assert lib.ep_expert_plan_destroy(eplan) == 0
+    assert lib.ep_plan_destroy(plan) == 0
