@@ -811,6 +811,53 @@ class EpDispatchCombineOp:
             ex["plan"], ctypes.byref(c[1]), _stream(stream, self._dev_index)))
         return self.combine_out
 
+    def expert_mlp(self, packed_recv_x, packed_recv_count, gate_up, gate_up_scales, down,
+                   down_scales, stream=None):
+        """The experts between dispatch_standard_moe (or
+        convert_dispatch_output) and combine_standard_moe (or
+        convert_combine_input): y = (silu(x gate^T) * (x up^T)) down^T for
+        each expert's rows, as two grouped FP8 products with the hidden rows
+        in FP8 between them. The config must dispatch FP8 rows with FP32
+        scales per 128 elements (dispatch_dtype "fp8", scale_dim H / 128).
+        packed_recv_x (rows, scales) and packed_recv_count are the dispatch's;
+        gate_up [E, 2 I, H] holds each expert's I gate rows, then its I up
+        rows, down [E, H, I], both E4M3 with FP32 scales per 128 x 128 block
+        (gate_up_scales [E, 2 I / 128, H / 128], down_scales [E, ceil(H / 128),
+        I / 128]). Returns the experts' outputs [W, Er, cap, H] in the combine
+        type, a view of a buffer the next call overwrites; rows past an
+        expert's count are not written."""
+        cfg = self.cfg
+        H, cap = cfg.hidden_dim, self.expert_capacity
+        if (cfg.dispatch_dtype != EP_FP8_E4M3 or cfg.scale_type_size != 4 or
+                cfg.scale_dim * 128 != H):
+            raise ValueError("expert_mlp needs dispatch_dtype fp8 with scale_dim = H / 128 float32 "
+                             "scales")
+        if gate_up.dim() != 3 or gate_up.shape[1] % 256:
+            raise ValueError("gate_up must be [E, 2 I, H] with I a multiple of 128, not "
+                             f"{list(gate_up.shape)}")
+        rows, scales = packed_recv_x
+        W, Er = cfg.world_size, cfg.num_experts_per_rank
+        G, inter = W * Er, gate_up.shape[1] // 2
+        if tuple(gate_up.shape) != (G, 2 * inter, H) or tuple(down.shape) != (G, H, inter):
+            raise ValueError(f"gate_up and down must be {[G, 2 * inter, H]} and {[G, H, inter]}, "
+                             f"not {list(gate_up.shape)} and {list(down.shape)}")
+        ex = self._expert_state()
+        if ex.get("inter") != inter:
+            dev = self.workspace.device
+            ex["hidden"] = torch.empty((G, cap, inter), dtype=torch.uint8, device=dev)
+            ex["hidden_scales"] = torch.empty((G, cap, inter // 128), dtype=torch.float32,
+                                              device=dev)
+            ex["mlp_y"] = torch.empty((W, Er, cap, H), dtype=_TORCH[cfg.combine_dtype],
+                                      device=dev)
+            ex["inter"] = inter
+        counts = packed_recv_count.view(G)
+        moe_grouped_gemm_swiglu(rows.view(G, cap, H), scales.view(torch.float32).view(
+            G, cap, H // 128), gate_up, gate_up_scales, ex["hidden"], ex["hidden_scales"], counts,
+            stream)
+        moe_grouped_gemm(ex["hidden"], ex["hidden_scales"], down, down_scales,
+                         ex["mlp_y"].view(G, cap, H), counts, stream)
+        return ex["mlp_y"]
+
     def combine_standard_moe_backward(self, grad_out, weights, indices, packed_y=None,
                                       grad_packed_y=None, grad_weights=None, stream=None):
         """Gradient of combine_standard_moe for the last dispatch_standard_moe:
@@ -876,5 +923,6 @@ class EpDispatchCombineOp:
             pass
 
 
-from .moe import (MOE_EXPORTED, MOE_FP32, moe_combine_backward, moe_dispatch_backward,  # noqa: E402
-                  moe_rms_norm)
+from .moe import (MOE_EPILOGUE_ROWS, MOE_EPILOGUE_SWIGLU, MOE_EXPORTED,  # noqa: E402
+                  MOE_FP32, moe_combine_backward, moe_dispatch_backward, moe_grouped_gemm,
+                  moe_grouped_gemm_swiglu, moe_rms_norm)

@@ -22,6 +22,9 @@ constexpr size_t kPtrAlign = 16;
 // last-level cache of an MI355X.
 constexpr int64_t kKeepBytes = 256ll << 20;
 
+// Blocks of a grouped product: one a compute unit of an MI355X.
+constexpr int kGemmBlocks = 256;
+
 int fail(int code, const char* fmt, ...)
 {
     char buf[512];
@@ -147,6 +150,63 @@ int moe_rms_norm(const moe_rms_norm_args_t* a, void* stream_ptr)
                                           streaming, static_cast<hipStream_t>(stream_ptr));
     if (e != hipSuccess)
         return fail(EP_ERR_HIP, "rms_norm launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int moe_grouped_gemm(const moe_grouped_gemm_args_t* a, void* stream_ptr)
+{
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    const bool swiglu = a->epilogue == MOE_EPILOGUE_SWIGLU;
+    if (!swiglu && a->epilogue != MOE_EPILOGUE_ROWS)
+        return fail(EP_ERR_ARG, "args.epilogue = %d: must be a MOE_EPILOGUE_* value", a->epilogue);
+    if (swiglu ? a->out_dtype != EP_FP8_E4M3
+               : a->out_dtype != EP_BF16 && a->out_dtype != EP_FP16)
+        return fail(EP_ERR_ARG, "args.out_dtype = %d: must be %s", a->out_dtype,
+                    swiglu ? "EP_FP8_E4M3 with MOE_EPILOGUE_SWIGLU" : "EP_BF16 or EP_FP16");
+    if (a->groups < 0 || a->cap < 0)
+        return fail(EP_ERR_ARG, "args.groups = %d, args.cap = %d: must be >= 0", a->groups, a->cap);
+    if (a->k < 128 || a->k % 128)
+        return fail(EP_ERR_ARG, "args.k = %d: must be a positive multiple of 128", a->k);
+    const int step = swiglu ? 256 : 8;
+    if (a->n < step || a->n % step)
+        return fail(EP_ERR_ARG, "args.n = %d: must be a positive multiple of %d", a->n, step);
+    if (a->n > (1 << 20) || a->k > (1 << 20))
+        return fail(EP_ERR_SIZE, "args.n = %d, args.k = %d: must be at most 2^20", a->n, a->k);
+    if ((int64_t)a->groups * a->cap > INT32_MAX)
+        return fail(EP_ERR_SIZE, "args.groups * args.cap = %lld exceeds 2^31 - 1",
+                    (long long)a->groups * a->cap);
+    if (a->groups == 0 || a->cap == 0)
+        return ok();
+    if (!swiglu && a->out_scales)
+        return fail(EP_ERR_ARG, "args.out_scales must be NULL with MOE_EPILOGUE_ROWS");
+    const Pointer ptrs[] = {{a->a, "args.a", kPtrAlign, true},
+                            {a->a_scales, "args.a_scales", 4, true},
+                            {a->b, "args.b", kPtrAlign, true},
+                            {a->b_scales, "args.b_scales", 4, true},
+                            {a->counts, "args.counts", 4, false},
+                            {a->out, "args.out", kPtrAlign, true},
+                            {a->out_scales, "args.out_scales", 4, swiglu}};
+    const int rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+    moe::GemmArgs ga;
+    ga.a = static_cast<const uint8_t*>(a->a);
+    ga.as = reinterpret_cast<const uint8_t*>(a->a_scales);
+    ga.b = static_cast<const uint8_t*>(a->b);
+    ga.bs = a->b_scales;
+    ga.counts = a->counts;
+    ga.out = static_cast<uint8_t*>(a->out);
+    ga.osc = reinterpret_cast<uint8_t*>(a->out_scales);
+    ga.groups = a->groups;
+    ga.cap = a->cap;
+    ga.n = a->n;
+    ga.k = a->k;
+    ga.col_tiles = (a->n + 255) / 256;
+    const hipError_t e = moe::launch_gemm(ga, a->out_dtype == EP_FP16 ? 1 : 0, swiglu, kGemmBlocks,
+                                          static_cast<hipStream_t>(stream_ptr));
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "grouped_gemm launch failed: %s", hipGetErrorString(e));
     return ok();
 }
 

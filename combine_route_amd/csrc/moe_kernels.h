@@ -74,4 +74,19 @@ hipError_t launch_combine_backward(const CombineBackwardArgs& a, const ep::Token
 hipError_t launch_dispatch_backward(const DispatchBackwardArgs& a, const ep::TokenMap& tk,
                                     int dtype, int waves, bool stream, hipStream_t s);
 
+// moe_gemm.hip: the grouped FP8 product.
+struct GemmArgs {
+    const uint8_t* a;            // [groups][cap][k] E4M3
+    const uint8_t* as;           // [groups][cap][k / 128] float
+    const uint8_t* b;            // [groups][n][k] E4M3
+    const float* bs;             // [groups][ceil(n / 128)][k / 128]
+    const int32_t* counts;       // [groups] or null
+    uint8_t* out;                // [groups][cap][n] bf16 / fp16, or [groups][cap][n / 2] E4M3
+    uint8_t* osc;                // [groups][cap][n / 256] float (swiglu)
+    int32_t groups, cap, n, k;
+    int32_t col_tiles;           // ceil(n / 256)
+};
+
+hipError_t launch_gemm(const GemmArgs& a, int dtype, bool swiglu, int blocks, hipStream_t s);
+
 }  // namespace moe

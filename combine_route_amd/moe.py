@@ -10,11 +10,13 @@ from typing import Optional
 
 import torch
 
-from . import (_F32, _I32, _TORCH, EP_BF16, EP_FP16, EpConfig, _check, _dev, _sizes, _stream,
-               load)
+from . import (_F32, _I32, _TORCH, EP_BF16, EP_FP16, EP_FP8_E4M3, EpConfig, _check, _dev,
+               _sizes, _stream, load)
 
 MOE_FP32 = 3
-MOE_EXPORTED = ("moe_rms_norm", "moe_combine_backward", "moe_dispatch_backward")
+MOE_EPILOGUE_ROWS, MOE_EPILOGUE_SWIGLU = 0, 1
+MOE_EXPORTED = ("moe_rms_norm", "moe_grouped_gemm", "moe_combine_backward",
+                "moe_dispatch_backward")
 
 _DTYPE_CODE = {torch.bfloat16: EP_BF16, torch.float16: EP_FP16}
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -25,6 +27,12 @@ class MoeRmsNormArgs(ctypes.Structure):
         "x", "residual", "residual_out", "weight", "out", "codes", "scales", "row_counts")] +
         [("rows", ctypes.c_int64), ("group_rows", ctypes.c_int64), ("hidden", ctypes.c_int32),
          ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float)])
+
+
+class MoeGroupedGemmArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "a", "a_scales", "b", "b_scales", "counts", "out", "out_scales")] +
+        [(n, ctypes.c_int32) for n in ("groups", "cap", "n", "k", "out_dtype", "epilogue")])
 
 
 class MoeCombineBackwardArgs(ctypes.Structure):
@@ -42,6 +50,7 @@ def _declare(lib):
         return lib
     V = ctypes.c_void_p
     lib.moe_rms_norm.argtypes = [ctypes.POINTER(MoeRmsNormArgs), V]
+    lib.moe_grouped_gemm.argtypes = [ctypes.POINTER(MoeGroupedGemmArgs), V]
     lib.moe_combine_backward.argtypes = [V, ctypes.POINTER(MoeCombineBackwardArgs), V]
     lib.moe_dispatch_backward.argtypes = [V, ctypes.POINTER(MoeDispatchBackwardArgs), V]
     for name in MOE_EXPORTED:
@@ -126,6 +135,54 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
         _shaped(counts, "counts", x.shape[:1], _I32), rows, group, H, dtype,
         MOE_FP32 if weight.dtype == torch.float32 else dtype, eps)
     _call("moe_rms_norm", index, stream, ctypes.byref(a))
+
+
+def _product_args(a, a_scales, b, b_scales, counts):
+    """Checked sizes and addresses of a grouped product's inputs."""
+    for t, name in ((a, "a"), (b, "b")):
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have 3 dimensions, not {t.dim()}")
+    groups, cap, k = a.shape
+    n = b.shape[1]
+    blocks = -(-k // 128)
+    return (groups, cap, n, k), (
+        _shaped(a, "a", (groups, cap, k), _CODES),
+        _shaped(a_scales, "a_scales", (groups, cap, blocks), _F32),
+        _shaped(b, "b", (groups, n, k), _CODES),
+        _shaped(b_scales, "b_scales", (groups, -(-n // 128), blocks), _F32),
+        _shaped(counts, "counts", (groups,), _I32))
+
+
+def moe_grouped_gemm(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
+                     b_scales: torch.Tensor, out: torch.Tensor,
+                     counts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_grouped_gemm() (include/moe.h) to bf16 / fp16 rows: a [G, cap, K]
+    E4M3 rows with a_scales [G, cap, K / 128], b [G, N, K] E4M3 weights with
+    b_scales [G, ceil(N / 128), K / 128]; out [G, cap, N]. counts: int32 [G]
+    rows of each group (default: cap)."""
+    index = _device_of(a=a, a_scales=a_scales, b=b, b_scales=b_scales, out=out, counts=counts)
+    (groups, cap, n, k), ptrs = _product_args(a, a_scales, b, b_scales, counts)
+    dtype = _DTYPE_CODE.get(out.dtype)
+    if dtype is None:
+        raise ValueError(f"out must be bf16 or fp16, not {out.dtype}")
+    args = MoeGroupedGemmArgs(*ptrs, _shaped(out, "out", (groups, cap, n), None), None, groups,
+                              cap, n, k, dtype, MOE_EPILOGUE_ROWS)
+    _call("moe_grouped_gemm", index, stream, ctypes.byref(args))
+
+
+def moe_grouped_gemm_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
+                            b_scales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                            counts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_grouped_gemm() (include/moe.h) with MOE_EPILOGUE_SWIGLU: b [G, 2 I,
+    K] holds each expert's I gate rows, then its I up rows; codes [G, cap, I]
+    and scales [G, cap, I / 128] get silu(gate) * up as E4M3."""
+    index = _device_of(a=a, a_scales=a_scales, b=b, b_scales=b_scales, codes=codes, scales=scales,
+                       counts=counts)
+    (groups, cap, n, k), ptrs = _product_args(a, a_scales, b, b_scales, counts)
+    args = MoeGroupedGemmArgs(*ptrs, _shaped(codes, "codes", (groups, cap, n // 2), _CODES),
+                              _shaped(scales, "scales", (groups, cap, n // 256), _F32), groups,
+                              cap, n, k, EP_FP8_E4M3, MOE_EPILOGUE_SWIGLU)
+    _call("moe_grouped_gemm", index, stream, ctypes.byref(args))
 
 
 def _packed_shape(cfg: EpConfig, cap: int):

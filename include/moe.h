@@ -83,6 +83,58 @@ typedef struct moe_rms_norm_args {
 
 int moe_rms_norm(const moe_rms_norm_args_t *args, void *stream);
 
+/* What moe_grouped_gemm does with the product. */
+enum {
+    MOE_EPILOGUE_ROWS = 0,   /* rows of bf16 / fp16                              */
+    MOE_EPILOGUE_SWIGLU = 1  /* FP8 rows of silu(gate) * up with block scales    */
+};
+
+/* Grouped product of expert-major FP8 rows with the experts' FP8 weights: for
+ * group g (an expert), row i < min(counts[g], cap) and weight row j,
+ *   y[g][i][j] = sum over blocks q of 128 elements of
+ *                a_scales[g][i][q] * b_scales[g][j / 128][q] *
+ *                sum over e in block q of a[g][i][e] * b[g][j][e]
+ * with every sum in FP32. MOE_EPILOGUE_ROWS rounds y once to out_dtype.
+ * MOE_EPILOGUE_SWIGLU takes weight rows [0, n / 2) as the gate and
+ * [n / 2, n) as the up projection, and quantizes z = gate / (1 + exp(-gate))
+ * * up (FP32) as above: the rows and scales of the next product.
+ *   a, a_scales   [groups][cap][k] E4M3, [groups][cap][k / 128] float: the
+ *                 packed rows and scales of an FP8 dispatch (packed_x and
+ *                 packed_scales with scale_dim = k / 128), or codes and
+ *                 scales of this call's swiglu form.
+ *   b, b_scales   [groups][n][k] E4M3, [groups][ceil(n / 128)][k / 128] float.
+ *   counts        device int32 [groups] (packed_count; a count above cap means
+ *                 cap, one below 0 none), or NULL: cap rows each.
+ *   out           ROWS: [groups][cap][n] of out_dtype (EP_BF16 or EP_FP16).
+ *                 SWIGLU: [groups][cap][n / 2] E4M3; out_dtype must be
+ *                 EP_FP8_E4M3.
+ *   out_scales    SWIGLU: [groups][cap][n / 256] float; else NULL.
+ * Rows past a group's count are neither read nor written. k: a positive
+ * multiple of 128; n: a positive multiple of 8 (ROWS) or 256 (SWIGLU); n and
+ * k at most 2^20, groups, cap >= 0. A row's result depends on its own inputs
+ * alone. a, b and out 16-byte aligned, the rest 4-byte.
+ * Errors: EP_ERR_NULL, EP_ERR_ALIGN, EP_ERR_ARG, EP_ERR_SIZE (n or k too
+ * large, groups * cap above 2^31 - 1, or more than 2^31 - 1 row tiles of 256),
+ * EP_ERR_HIP. groups == 0 or cap == 0 returns EP_OK whatever the pointers
+ * are. */
+typedef struct moe_grouped_gemm_args {
+    const void *a;
+    const float *a_scales;
+    const void *b;
+    const float *b_scales;
+    const int32_t *counts;
+    void *out;
+    float *out_scales;
+    int32_t groups;
+    int32_t cap;
+    int32_t n;
+    int32_t k;
+    int32_t out_dtype;
+    int32_t epilogue;
+} moe_grouped_gemm_args_t;
+
+int moe_grouped_gemm(const moe_grouped_gemm_args_t *args, void *stream);
+
 /* ------------------------------------------------------------------------
  * Gradients of the fused calls. Both use the map of the last
  * ep_dispatch_standard_moe on the expert plan, as ep_combine_standard_moe

@@ -1,0 +1,289 @@
+"""moe_grouped_gemm on the GPU against the plain 64-bit form.
+
+Bounds. The FP8 products are exact in binary32 (two 4-bit significands).
+  The swiglu form adds them in FP32. Any order of k additions and k / 128
+multiply-adds is within k + k / 64 half steps of the sum of magnitudes; of
+random signs, far inside: 4 sqrt(k) + 16 half steps, and 2 for the scales.
+  The form to bf16 / fp16 rows uses the FP8 matrix instruction, which adds 8
+products at a time, aligned to the largest of the 8 and cut below 2^-13 of it
+(measured on gfx950 with single products, in k positions of one 8 and of
+different ones). Of 8 products the 7 smaller ones then lose less than 7 * 2^-13
+of the largest, and the largest ones of all groups of 8 add up to no more than
+the sum of magnitudes: 7 * 2^-13 of it bounds the loss in any case. What is
+lost has random signs, so the whole output's error stays a rounding's: in the
+2-norm half a step of the output type."""
+import pytest
+import torch
+
+import combine_route_amd as cra
+import moe_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    cra.load()
+
+
+def inputs(G, cap, n, k, seed=0):
+    """Random codes (every finite magnitude of a normal draw) and scales, on
+    the CPU."""
+    g = torch.Generator().manual_seed(seed)
+    a = (60 * torch.randn((G, cap, k), generator=g)).clamp(-448, 448).to(ref.E4M3)
+    b = (60 * torch.randn((G, n, k), generator=g)).clamp(-448, 448).to(ref.E4M3)
+    sa = (0.5 + torch.rand((G, cap, k // 128), generator=g)) / 60
+    sb = (0.5 + torch.rand((G, -(-n // 128), k // 128), generator=g)) / 60 / k ** 0.5
+    return a, sa, b, sb
+
+
+def product(a, sa, b, sb):
+    """(y, sum of magnitudes) in 64 bits."""
+    A = a.double() * sa.double().repeat_interleave(128, -1)
+    B = b.double() * sb.double().repeat_interleave(128, 1)[:, :b.shape[1]].repeat_interleave(
+        128, -1)
+    B = B.transpose(1, 2).contiguous()
+    return torch.matmul(A, B), torch.matmul(A.abs(), B.abs())
+
+
+def slack(k):
+    return (4 * k ** 0.5 + 18) * ref.F32
+
+
+CUT = 7 * 2.0 ** -13
+
+
+def counted(counts, G, cap):
+    return [cap] * G if counts is None else [max(0, min(cap, c)) for c in counts]
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def run_rows(inp, counts, dtype, stream=None):
+    a, sa, b, sb = inp
+    out = torch.full((a.shape[0], a.shape[1], b.shape[1]), 7.0, dtype=dtype, device="cuda")
+    cra.moe_grouped_gemm(dev(a), dev(sa), dev(b), dev(sb), out, counts=counts, stream=stream)
+    return out
+
+
+def run_swiglu(inp, counts):
+    a, sa, b, sb = inp
+    G, cap, inter = a.shape[0], a.shape[1], b.shape[1] // 2
+    codes = torch.full((G, cap, inter), 77, dtype=torch.uint8, device="cuda")
+    scales = torch.full((G, cap, inter // 128), 7.0, device="cuda")
+    cra.moe_grouped_gemm_swiglu(dev(a), dev(sa), dev(b), dev(sb), codes, scales, counts=counts)
+    return codes, scales
+
+
+def device_counts(counts):
+    return None if counts is None else torch.tensor(counts, dtype=torch.int32, device="cuda")
+
+
+ROWS = [
+    dict(G=1, cap=1, n=8, k=128, counts=None),
+    dict(G=1, cap=1, n=256, k=256, counts=None),
+    dict(G=3, cap=5, n=24, k=384, counts=[5, 0, 3]),
+    dict(G=8, cap=32, n=256, k=256, counts=[8, 0, 1, 32, 40, 5, 16, -2]),
+    dict(G=2, cap=70, n=136, k=640, counts=[70, 65]),
+    dict(G=3, cap=150, n=520, k=512, counts=[128, 129, 64]),
+    dict(G=2, cap=700, n=264, k=256, counts=[700, 513]),
+    dict(G=4, cap=300, n=1000, k=1024, counts=[257, 256, 255, 300]),
+    dict(G=2, cap=64, n=7168, k=2048, counts=[33, 64]),
+    dict(G=1, cap=40, n=512, k=7168, counts=None),
+    dict(G=700, cap=3, n=16, k=128, counts=[(7 * i) % 5 for i in range(700)]),
+    dict(G=5, cap=9, n=128, k=128, counts=[0] * 5),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", ROWS, ids=lambda c: f"G{c['G']}-cap{c['cap']}-n{c['n']}-k{c['k']}")
+def test_rows(case, dtype):
+    G, cap, n, k, counts = (case[x] for x in ("G", "cap", "n", "k", "counts"))
+    inp = inputs(G, cap, n, k)
+    out = run_rows(inp, device_counts(counts), TYPES[dtype]).cpu()
+    y, size = product(*inp)
+    for g, c in enumerate(counted(counts, G, cap)):
+        ref.close_to(out[g, :c], y[g, :c], TYPES[dtype], 0.0, (CUT + slack(k)) * size[g, :c])
+        off = (out[g, :c].double() - y[g, :c]).norm()
+        assert float(off) <= ref.half_step(TYPES[dtype]) * float(y[g, :c].norm())
+        assert bool((out[g, c:] == 7).all())
+
+
+SWIGLU = [
+    dict(G=1, cap=1, n=256, k=128, counts=None),
+    dict(G=2, cap=37, n=512, k=384, counts=[37, 2]),
+    dict(G=4, cap=140, n=768, k=512, counts=[0, 100, 140, 999]),
+    dict(G=2, cap=400, n=256, k=1024, counts=[300, 390]),
+    dict(G=1, cap=20, n=4096, k=1024, counts=None),
+]
+
+
+def swiglu(y, size, k):
+    """(z, its FP32 error bound): with e the error of gate and up, |dz| <= |dz
+    / dgate| e + |silu(gate)| e, |d silu| <= 1.1, and the FP32 arithmetic: the
+    exponential of -gate to 2 + |gate| half steps (its argument is rounded
+    after a product), sum, reciprocal and two products 6 more."""
+    inter = y.shape[-1] // 2
+    gate, up = y[..., :inter], y[..., inter:]
+    e = slack(k) * size
+    silu = gate * torch.sigmoid(gate)
+    z = silu * up
+    return z, 1.1 * e[..., :inter] * up.abs() + silu.abs() * e[..., inter:] + \
+        (8 + gate.abs()) * ref.F32 * z.abs()
+
+
+@pytest.mark.parametrize("case", SWIGLU,
+                         ids=lambda c: f"G{c['G']}-cap{c['cap']}-n{c['n']}-k{c['k']}")
+def test_swiglu(case):
+    G, cap, n, k, counts = (case[x] for x in ("G", "cap", "n", "k", "counts"))
+    inp = inputs(G, cap, n, k, seed=1)
+    codes, scales = (v.cpu() for v in run_swiglu(inp, device_counts(counts)))
+    z, err = swiglu(*product(*inp), k)
+    for g, c in enumerate(counted(counts, G, cap)):
+        if c:
+            ref.quantized_close(codes[g, :c], scales[g, :c], z[g, :c], 0.0, err[g, :c])
+        assert bool((codes[g, c:] == 77).all()) and bool((scales[g, c:] == 7).all())
+
+
+def test_each_operand_element_meets_its_own():
+    """One nonzero element a row on either side, so every product of the
+    matrix instruction's lanes and chunks shows on its own."""
+    k, cap, n = 256, 256, 256
+    a = torch.zeros((1, cap, k))
+    b = torch.zeros((1, n, k))
+    i = torch.arange(256)
+    a[0, i, i] = 1.0
+    a[0, i, (i * 7 + 3) % k] = 2.0
+    b[0, i, (i * 5 + 1) % k] = 1.0
+    b[0, i, (i * 11 + 4) % k] = -4.0
+    sa = 2.0 ** (torch.arange(cap * 2) % 5 - 2).view(1, cap, 2)
+    sb = 2.0 ** torch.tensor([[[0., 1.], [-1., 2.]]])
+    inp = a.to(ref.E4M3), sa, b.to(ref.E4M3), sb
+    out = run_rows(inp, None, torch.bfloat16).cpu()
+    assert torch.equal(out.double(), product(*inp)[0])
+
+
+def test_special_values_stay_in_their_rows():
+    inp = inputs(2, 70, 264, 256, seed=2)
+    want = run_rows(inp, None, torch.bfloat16)
+    a, sa, b, sb = (v.clone() for v in inp)
+    a.view(torch.uint8)[0, 3, 100] = 0x7F          # NaN
+    sa[1, 69, 1] = float("inf")
+    b.view(torch.uint8)[1, 200, 0] = 0xFF          # NaN weight
+    got = run_rows((a, sa, b, sb), None, torch.bfloat16)
+    assert bool(got[0, 3].isnan().all()) and bool(got[1, :, 200].isnan().all())
+    assert not bool(got[1, 69].isfinite().any())
+    rest = torch.ones_like(got, dtype=torch.bool)
+    rest[0, 3] = rest[1, 69] = False
+    rest[1, :, 200] = False
+    assert torch.equal(got[rest], want[rest])
+
+
+def test_rows_past_the_count_are_not_read():
+    inp = inputs(2, 300, 256, 256, seed=3)
+    counts = device_counts([130, 7])
+    want = run_rows(inp, counts, torch.float16)
+    a, sa = inp[0].clone(), inp[1].clone()
+    for g, c in enumerate((130, 7)):
+        a.view(torch.uint8)[g, c:] = 0x7F
+        sa[g, c:] = float("nan")
+    got = run_rows((a, sa) + inp[2:], counts, torch.float16)
+    assert torch.equal(got, want)
+
+
+def test_a_row_does_not_depend_on_the_call():
+    """The same bits whatever tile a row falls in."""
+    inp = inputs(1, 600, 512, 1024, seed=4)
+    want = run_rows(inp, None, torch.bfloat16)
+    wc, ws = run_swiglu(inp, None)
+    for lo, hi in ((0, 1), (5, 60), (100, 220), (300, 600)):
+        part = (inp[0][:, lo:hi].contiguous(), inp[1][:, lo:hi].contiguous()) + inp[2:]
+        assert torch.equal(run_rows(part, None, torch.bfloat16), want[:, lo:hi])
+        c, s = run_swiglu(part, None)
+        assert torch.equal(c, wc[:, lo:hi]) and torch.equal(s, ws[:, lo:hi])
+
+
+def test_zero_rows_get_scale_one():
+    a, sa, b, sb = inputs(1, 5, 256, 128, seed=5)
+    a[0, 2] = 0
+    codes, scales = run_swiglu((a, sa, b, sb), None)
+    assert float(scales[0, 2, 0]) == 1.0 and bool((codes[0, 2] & 0x7F == 0).all())
+
+
+def test_binding_refuses():
+    a, sa, b, sb = (v.cuda() for v in inputs(2, 16, 256, 256))
+    out = torch.empty((2, 16, 256), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="a_scales"):
+        cra.moe_grouped_gemm(a, sa[..., :1].contiguous(), b, sb, out)
+    with pytest.raises(ValueError, match="b_scales"):
+        cra.moe_grouped_gemm(a, sa, b, sb[:, :1].contiguous(), out)
+    with pytest.raises(ValueError, match="b must be"):
+        cra.moe_grouped_gemm(a, sa, b[:1].contiguous(), sb, out)
+    with pytest.raises(ValueError, match="out"):
+        cra.moe_grouped_gemm(a, sa, b, sb, out.float())
+    with pytest.raises(ValueError, match="out"):
+        cra.moe_grouped_gemm(a, sa, b, sb, out[:, :8].contiguous())
+    with pytest.raises(ValueError, match="a must be"):
+        cra.moe_grouped_gemm(a.float(), sa, b, sb, out)
+    with pytest.raises(ValueError, match="counts"):
+        cra.moe_grouped_gemm(a, sa, b, sb, out, counts=torch.zeros(2, device="cuda"))
+    with pytest.raises(ValueError, match="3 dimensions"):
+        cra.moe_grouped_gemm(a[0], sa[0], b, sb, out)
+    with pytest.raises(cra.EpError, match="args.k"):
+        cra.moe_grouped_gemm(a[..., :64].contiguous(), sa[..., :1].contiguous(),
+                             b[..., :64].contiguous(), sb[..., :1].contiguous(), out)
+    codes = torch.empty((2, 16, 128), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="scales"):
+        cra.moe_grouped_gemm_swiglu(a, sa, b, sb, codes, torch.empty((2, 16, 2), device="cuda"))
+
+
+def test_empty_calls():
+    a, sa, b, sb = (v.cuda() for v in inputs(2, 4, 256, 128))
+    cra.moe_grouped_gemm(a[:, :0].contiguous(), sa[:, :0].contiguous(), b, sb,
+                         torch.empty((2, 0, 256), dtype=torch.bfloat16, device="cuda"))
+    cra.moe_grouped_gemm(a[:0], sa[:0], b[:0], sb[:0],
+                         torch.empty((0, 4, 256), dtype=torch.bfloat16, device="cuda"))
+
+
+def test_streams_and_graph():
+    inp = inputs(4, 100, 512, 512, seed=6)
+    counts = device_counts([100, 0, 33, 64])
+    want = run_rows(inp, counts, torch.bfloat16)
+    wc, ws = run_swiglu(inp, counts)
+    a, sa, b, sb = (v.cuda() for v in inp)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.full_like(want, 7.0) for _ in streams]
+    out, codes, scales = torch.full_like(want, 7.0), torch.full_like(wc, 77), torch.full_like(ws, 7)
+    torch.cuda.synchronize()
+    for s, o in zip(streams, outs):
+        cra.moe_grouped_gemm(a, sa, b, sb, o, counts=counts, stream=s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cra.moe_grouped_gemm(a, sa, b, sb, out, counts=counts)
+        cra.moe_grouped_gemm_swiglu(a, sa, b, sb, codes, scales, counts=counts)
+    for _ in range(3):
+        out.fill_(7.0)
+        codes.fill_(77)
+        scales.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(codes, wc) and torch.equal(scales, ws)
+    for o in outs:
+        assert torch.equal(o, want)
+    # the counts are read when the graph runs
+    counts.copy_(torch.tensor([1, 2, 3, 4], dtype=torch.int32))
+    out.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for g in range(4):
+        assert bool((out[g, g + 1:] == 7).all())
+        assert torch.equal(out[g, :g + 1][:int(min(g + 1, [100, 0, 33, 64][g]))],
+                           want[g, :g + 1][:int(min(g + 1, [100, 0, 33, 64][g]))])

@@ -133,3 +133,56 @@ def test_backward_calls_refuse(lib):
     assert lib.moe_dispatch_backward(eplan, ctypes.byref(db), None) == cra.EP_ERR_STATE
     assert lib.ep_expert_plan_destroy(eplan) == 0
     assert lib.ep_plan_destroy(plan) == 0
+
+
+def gemm_args(**kw):
+    a = dict(a=FAKE, a_scales=FAKE, b=FAKE, b_scales=FAKE, counts=FAKE, out=FAKE, out_scales=None,
+             groups=4, cap=64, n=256, k=256, out_dtype=cra.EP_BF16,
+             epilogue=cra.MOE_EPILOGUE_ROWS)
+    a.update(kw)
+    return moe.MoeGroupedGemmArgs(**a)
+
+
+SWIGLU = dict(epilogue=cra.MOE_EPILOGUE_SWIGLU, out_dtype=cra.EP_FP8_E4M3, out_scales=FAKE)
+BAD_GEMM = [
+    (dict(a=None), cra.EP_ERR_NULL, "args.a "),
+    (dict(a_scales=None), cra.EP_ERR_NULL, "a_scales"),
+    (dict(b=None), cra.EP_ERR_NULL, "args.b "),
+    (dict(b_scales=None), cra.EP_ERR_NULL, "b_scales"),
+    (dict(out=None), cra.EP_ERR_NULL, "out"),
+    (dict(SWIGLU, out_scales=None), cra.EP_ERR_NULL, "out_scales"),
+    (dict(out_scales=FAKE), cra.EP_ERR_ARG, "out_scales"),
+    (dict(a=FAKE + 8), cra.EP_ERR_ALIGN, "args.a "),
+    (dict(b=FAKE + 4), cra.EP_ERR_ALIGN, "args.b "),
+    (dict(out=FAKE + 8), cra.EP_ERR_ALIGN, "out"),
+    (dict(a_scales=FAKE + 2), cra.EP_ERR_ALIGN, "a_scales"),
+    (dict(b_scales=FAKE + 2), cra.EP_ERR_ALIGN, "b_scales"),
+    (dict(counts=FAKE + 2), cra.EP_ERR_ALIGN, "counts"),
+    (dict(SWIGLU, out_scales=FAKE + 2), cra.EP_ERR_ALIGN, "out_scales"),
+    (dict(groups=-1), cra.EP_ERR_ARG, "groups"),
+    (dict(cap=-1), cra.EP_ERR_ARG, "cap"),
+    (dict(k=0), cra.EP_ERR_ARG, "args.k"),
+    (dict(k=192), cra.EP_ERR_ARG, "args.k"),
+    (dict(n=0), cra.EP_ERR_ARG, "args.n"),
+    (dict(n=12), cra.EP_ERR_ARG, "args.n"),
+    (dict(SWIGLU, n=128), cra.EP_ERR_ARG, "256"),
+    (dict(n=(1 << 20) + 8), cra.EP_ERR_SIZE, "args.n"),
+    (dict(k=(1 << 20) + 128), cra.EP_ERR_SIZE, "args.k"),
+    (dict(groups=1 << 16, cap=1 << 16), cra.EP_ERR_SIZE, "groups"),
+    (dict(out_dtype=cra.EP_FP8_E4M3), cra.EP_ERR_ARG, "out_dtype"),
+    (dict(SWIGLU, out_dtype=cra.EP_BF16), cra.EP_ERR_ARG, "out_dtype"),
+    (dict(epilogue=2), cra.EP_ERR_ARG, "epilogue"),
+]
+
+
+@pytest.mark.parametrize("change,code,word", BAD_GEMM)
+def test_grouped_gemm_refuses(lib, change, code, word):
+    assert lib.moe_grouped_gemm(ctypes.byref(gemm_args(**change)), None) == code
+    assert word in cra.ep_last_error()
+
+
+def test_grouped_gemm_without_rows_is_no_work(lib):
+    assert lib.moe_grouped_gemm(None, None) == cra.EP_ERR_NULL
+    for change in (dict(groups=0), dict(cap=0)):
+        args = gemm_args(a=None, out=None, **change)
+        assert lib.moe_grouped_gemm(ctypes.byref(args), None) == cra.EP_OK
