@@ -4,14 +4,13 @@ tensor is checked to be a contiguous device tensor of the right element type
 and shape, all on one device, before a pointer reaches the library, and the
 call runs on that device, on the given stream or torch's current one there.
 """
-import contextlib
 import ctypes
 from typing import Optional
 
 import torch
 
-from . import (_F32, _I32, _TORCH, EP_BF16, EP_FP16, EP_FP8_E4M3, EpConfig, _check, _dev,
-               _sizes, _stream, load)
+from . import (_F32, _I32, _TORCH, EP_BF16, EP_FP16, EP_FP8_E4M3, EpConfig, _check, _stream,
+               load)
 
 MOE_FP32 = 3
 MOE_EPILOGUE_ROWS, MOE_EPILOGUE_SWIGLU = 0, 1
@@ -19,6 +18,7 @@ MOE_EXPORTED = ("moe_rms_norm", "moe_grouped_gemm", "moe_combine_backward",
                 "moe_dispatch_backward")
 
 _DTYPE_CODE = {torch.bfloat16: EP_BF16, torch.float16: EP_FP16}
+_ROWS = (torch.bfloat16, torch.float16)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
@@ -59,42 +59,64 @@ def _declare(lib):
     return lib
 
 
+_fns = {}
+
+
 def _lib():
-    return _declare(load())
+    """The library with its moe_ functions declared."""
+    if not _fns:
+        lib = _declare(load())
+        _fns.update((name, getattr(lib, name)) for name in MOE_EXPORTED)
+    return load()
 
 
-def _shaped(t: Optional[torch.Tensor], name: str, shape, dtypes):
-    """Address of a tensor that has exactly this shape; None stays None."""
+def _refuse(t, name, shape, dtypes, index):
+    """Says what is wrong with a tensor that _ptr does not accept."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU, not {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, shape, dtypes, index: int):
+    """Address of a contiguous tensor of exactly this shape, one of these
+    element types and on device `index`; None stays None."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    nbytes = t.numel() * t.element_size() if isinstance(t, torch.Tensor) else 0
-    return _dev(t, name, nbytes, dtypes)
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == index and
+            t.shape == shape and t.dtype in dtypes and t.is_contiguous()):
+        _refuse(t, name, shape, dtypes, index)
+    return t.data_ptr()
 
 
-def _device_of(**tensors) -> int:
-    """The one device all of a call's tensors are on."""
-    index = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} must be on the GPU, not {t.device}")
-        if index is None:
-            index = t.device.index
-        elif t.device.index != index:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
-    return index
+def _index_of(t, name: str) -> int:
+    """The device a call runs on: its first tensor's."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU, not {t.device}")
+    return t.get_device()
 
 
 def _call(fn, index, stream, *args):
-    """One library call with `index` the current device."""
-    other = torch.cuda.current_device() != index
-    with torch.cuda.device(index) if other else contextlib.nullcontext():
-        _check(fn, getattr(_lib(), fn)(*args, _stream(stream, index)))
+    """One library call with `index` the current device, on the given stream
+    or torch's current one there."""
+    if not _fns:
+        _lib()
+    if torch.cuda.current_device() == index:
+        rc = _fns[fn](*args, _stream(stream, index))
+    else:
+        with torch.cuda.device(index):
+            rc = _fns[fn](*args, _stream(stream, index))
+    if rc:
+        _check(fn, rc)
 
 
 def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
@@ -109,48 +131,51 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
     the same rows as E4M3 with a scale per 128 elements. counts: an int32
     tensor of one count per leading index of x ([G, R, H] rows with counts
     [G]); only the first counts[g] rows of group g are read and written."""
-    index = _device_of(x=x, weight=weight, out=out, residual=residual, residual_out=residual_out,
-                       codes=codes, scales=scales, counts=counts)
+    index = _index_of(x, "x")
+    _index_of(weight, "weight")
     dtype = _DTYPE_CODE.get(x.dtype)
     if dtype is None:
         raise ValueError(f"x must be bf16 or fp16, not {x.dtype}")
-    if x.dim() < 1 or x.shape[-1] == 0:
+    shape = x.shape
+    H = shape[-1] if shape else 0
+    if H == 0:
         raise ValueError("x must have rows of at least one element")
-    H = x.shape[-1]
     rows = x.numel() // H
     if residual is not None and residual_out is None:
         residual_out = residual
     same = (x.dtype,)
     group = 0
     if counts is not None:
-        if x.dim() < 2 or x.shape[0] == 0:
+        if len(shape) < 2 or shape[0] == 0:
             raise ValueError("counts needs rows of shape [G, ..., H] with G >= 1")
-        group = max(1, rows // x.shape[0])
+        group = max(1, rows // shape[0])
     a = MoeRmsNormArgs(
-        _shaped(x, "x", x.shape, same), _shaped(residual, "residual", x.shape, same),
-        _shaped(residual_out, "residual_out", x.shape, same),
-        _shaped(weight, "weight", (H,), (x.dtype, torch.float32)),
-        _shaped(out, "out", x.shape, same), _shaped(codes, "codes", x.shape, _CODES),
-        _shaped(scales, "scales", x.shape[:-1] + (H // 128,), _F32),
-        _shaped(counts, "counts", x.shape[:1], _I32), rows, group, H, dtype,
-        MOE_FP32 if weight.dtype == torch.float32 else dtype, eps)
+        _ptr(x, "x", shape, same, index), _ptr(residual, "residual", shape, same, index),
+        _ptr(residual_out, "residual_out", shape, same, index),
+        _ptr(weight, "weight", (H,), (x.dtype, torch.float32), index),
+        _ptr(out, "out", shape, same, index), _ptr(codes, "codes", shape, _CODES, index),
+        _ptr(scales, "scales", shape[:-1] + (H // 128,), _F32, index),
+        _ptr(counts, "counts", shape[:1], _I32, index), rows, group, H, dtype,
+        dtype if weight.dtype == x.dtype else MOE_FP32, eps)
     _call("moe_rms_norm", index, stream, ctypes.byref(a))
 
 
 def _product_args(a, a_scales, b, b_scales, counts):
-    """Checked sizes and addresses of a grouped product's inputs."""
+    """Device, checked sizes and addresses of a grouped product's inputs."""
+    index = _index_of(a, "a")
+    _index_of(b, "b")
     for t, name in ((a, "a"), (b, "b")):
         if t.dim() != 3:
             raise ValueError(f"{name} must have 3 dimensions, not {t.dim()}")
     groups, cap, k = a.shape
     n = b.shape[1]
     blocks = -(-k // 128)
-    return (groups, cap, n, k), (
-        _shaped(a, "a", (groups, cap, k), _CODES),
-        _shaped(a_scales, "a_scales", (groups, cap, blocks), _F32),
-        _shaped(b, "b", (groups, n, k), _CODES),
-        _shaped(b_scales, "b_scales", (groups, -(-n // 128), blocks), _F32),
-        _shaped(counts, "counts", (groups,), _I32))
+    return index, (groups, cap, n, k), (
+        _ptr(a, "a", a.shape, _CODES, index),
+        _ptr(a_scales, "a_scales", (groups, cap, blocks), _F32, index),
+        _ptr(b, "b", (groups, n, k), _CODES, index),
+        _ptr(b_scales, "b_scales", (groups, -(-n // 128), blocks), _F32, index),
+        _ptr(counts, "counts", (groups,), _I32, index))
 
 
 def moe_grouped_gemm(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
@@ -160,13 +185,10 @@ def moe_grouped_gemm(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
     E4M3 rows with a_scales [G, cap, K / 128], b [G, N, K] E4M3 weights with
     b_scales [G, ceil(N / 128), K / 128]; out [G, cap, N]. counts: int32 [G]
     rows of each group (default: cap)."""
-    index = _device_of(a=a, a_scales=a_scales, b=b, b_scales=b_scales, out=out, counts=counts)
-    (groups, cap, n, k), ptrs = _product_args(a, a_scales, b, b_scales, counts)
-    dtype = _DTYPE_CODE.get(out.dtype)
-    if dtype is None:
-        raise ValueError(f"out must be bf16 or fp16, not {out.dtype}")
-    args = MoeGroupedGemmArgs(*ptrs, _shaped(out, "out", (groups, cap, n), None), None, groups,
-                              cap, n, k, dtype, MOE_EPILOGUE_ROWS)
+    index, (groups, cap, n, k), ptrs = _product_args(a, a_scales, b, b_scales, counts)
+    _index_of(out, "out")
+    args = MoeGroupedGemmArgs(*ptrs, _ptr(out, "out", (groups, cap, n), _ROWS, index), None,
+                              groups, cap, n, k, _DTYPE_CODE[out.dtype], MOE_EPILOGUE_ROWS)
     _call("moe_grouped_gemm", index, stream, ctypes.byref(args))
 
 
@@ -176,42 +198,37 @@ def moe_grouped_gemm_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Te
     """moe_grouped_gemm() (include/moe.h) with MOE_EPILOGUE_SWIGLU: b [G, 2 I,
     K] holds each expert's I gate rows, then its I up rows; codes [G, cap, I]
     and scales [G, cap, I / 128] get silu(gate) * up as E4M3."""
-    index = _device_of(a=a, a_scales=a_scales, b=b, b_scales=b_scales, codes=codes, scales=scales,
-                       counts=counts)
-    (groups, cap, n, k), ptrs = _product_args(a, a_scales, b, b_scales, counts)
-    args = MoeGroupedGemmArgs(*ptrs, _shaped(codes, "codes", (groups, cap, n // 2), _CODES),
-                              _shaped(scales, "scales", (groups, cap, n // 256), _F32), groups,
-                              cap, n, k, EP_FP8_E4M3, MOE_EPILOGUE_SWIGLU)
+    index, (groups, cap, n, k), ptrs = _product_args(a, a_scales, b, b_scales, counts)
+    args = MoeGroupedGemmArgs(*ptrs, _ptr(codes, "codes", (groups, cap, n // 2), _CODES, index),
+                              _ptr(scales, "scales", (groups, cap, n // 256), _F32, index),
+                              groups, cap, n, k, EP_FP8_E4M3, MOE_EPILOGUE_SWIGLU)
     _call("moe_grouped_gemm", index, stream, ctypes.byref(args))
-
-
-def _packed_shape(cfg: EpConfig, cap: int):
-    return (cfg.world_size, cfg.num_experts_per_rank, cap, cfg.hidden_dim)
 
 
 def moe_combine_backward(eplan: int, cfg: EpConfig, cap: int, grad_out, indices, weights, packed_y,
                          grad_packed_y, grad_weights, stream=None) -> None:
     """moe_combine_backward(); tensors as in include/moe.h."""
-    index = _device_of(grad_out=grad_out, indices=indices, weights=weights, packed_y=packed_y,
-                       grad_packed_y=grad_packed_y, grad_weights=grad_weights)
-    W, M, k, _, _, _ = _sizes(cfg)
-    rows, slots = (W, M, cfg.hidden_dim), (W, M, k)
-    packed, dt = _packed_shape(cfg, cap), (_TORCH[cfg.combine_dtype],)
+    index = _index_of(grad_out, "grad_out")
+    W, M, k, H = (cfg.world_size, cfg.max_num_inp_token_per_rank, cfg.num_experts_per_token,
+                  cfg.hidden_dim)
+    slots, packed = (W, M, k), (W, cfg.num_experts_per_rank, cap, H)
+    dt = (_TORCH[cfg.combine_dtype],)
     a = MoeCombineBackwardArgs(
-        _shaped(grad_out, "grad_out", rows, dt), _shaped(indices, "indices", slots, _I32),
-        _shaped(weights, "weights", slots, _F32), _shaped(packed_y, "packed_y", packed, dt),
-        _shaped(grad_packed_y, "grad_packed_y", packed, dt),
-        _shaped(grad_weights, "grad_weights", slots, _F32))
+        _ptr(grad_out, "grad_out", (W, M, H), dt, index),
+        _ptr(indices, "indices", slots, _I32, index), _ptr(weights, "weights", slots, _F32, index),
+        _ptr(packed_y, "packed_y", packed, dt, index),
+        _ptr(grad_packed_y, "grad_packed_y", packed, dt, index),
+        _ptr(grad_weights, "grad_weights", slots, _F32, index))
     _call("moe_combine_backward", index, stream, eplan, ctypes.byref(a))
 
 
 def moe_dispatch_backward(eplan: int, cfg: EpConfig, cap: int, grad_packed_x, grad_x,
                           stream=None) -> None:
     """moe_dispatch_backward(); tensors as in include/moe.h."""
-    index = _device_of(grad_packed_x=grad_packed_x, grad_x=grad_x)
-    W, M, _, _, _, _ = _sizes(cfg)
+    index = _index_of(grad_packed_x, "grad_packed_x")
+    W, H = cfg.world_size, cfg.hidden_dim
     dt = (_TORCH[cfg.combine_dtype],)
     a = MoeDispatchBackwardArgs(
-        _shaped(grad_packed_x, "grad_packed_x", _packed_shape(cfg, cap), dt),
-        _shaped(grad_x, "grad_x", (W, M, cfg.hidden_dim), dt))
+        _ptr(grad_packed_x, "grad_packed_x", (W, cfg.num_experts_per_rank, cap, H), dt, index),
+        _ptr(grad_x, "grad_x", (W, cfg.max_num_inp_token_per_rank, H), dt, index))
     _call("moe_dispatch_backward", index, stream, eplan, ctypes.byref(a))

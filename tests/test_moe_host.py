@@ -91,8 +91,17 @@ def test_tensors_off_the_gpu_are_refused():
     x = torch.zeros((2, 128), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU"):
         cra.moe_rms_norm(x, torch.ones(128, dtype=torch.bfloat16), 1e-6, out=x)
+    with pytest.raises(TypeError, match="x must"):
+        cra.moe_rms_norm([1.0], x, 1e-6)
     with pytest.raises(TypeError, match="weight"):
-        moe._device_of(weight=[1.0])
+        moe._refuse([1.0], "weight", (1,), (torch.float32,), 0)
+    with pytest.raises(ValueError, match="GPU"):
+        cra.moe_grouped_gemm(x, x, x, x, x)
+    cfg = cra.make_config(2, 128, 4, 2, 2)
+    with pytest.raises(ValueError, match="GPU"):
+        cra.moe_dispatch_backward(0, cfg, 4, x, x)
+    with pytest.raises(ValueError, match="GPU"):
+        cra.moe_combine_backward(0, cfg, 4, x, x, None, None, x, None)
 
 
 def test_backward_calls_refuse(lib):
