@@ -62,33 +62,41 @@ constexpr int kSubs = kWaveRows / 16;           // 16-row operands of them
 constexpr int kBLoads = kTileN / 64;            // 16-byte loads a lane and weight slice
 
 // Token rows of a tile whose waves hold TS operands of 16 rows each, and its
-// place in LDS: S slices of the rows, S of the weights, and two blocks of
-// scales (4 steps of every row, then of the tile's two weight blocks).
+// place in LDS: kAStages slices of the rows, b_stages of the weights, and two
+// blocks of scales (4 steps of every row, then of the tile's two weight
+// blocks).
+constexpr int kMaxTS = 7;
 constexpr int tile_rows(int ts) { return 2 * 16 * ts; }
-constexpr int stages(int ts) { return ts == 8 ? 2 : 3; }
+constexpr int kTileRows = tile_rows(kMaxTS);
+constexpr int kAStages = 3;
+constexpr int b_stages(int ts) { return ts == 7 ? 2 : ts == 4 ? 3 : 4; }
 constexpr int a_bytes(int ts) { return tile_rows(ts) * kSlice; }
 constexpr int kBBytes = kTileN * kSlice;
-constexpr int scale_bytes(int ts) { return (tile_rows(ts) + 64) * 16; }
-constexpr int lds_bytes(int ts) { return stages(ts) * (a_bytes(ts) + kBBytes) + 2 * scale_bytes(ts); }
-constexpr int kLdsBytes = lds_bytes(4);
-static_assert(lds_bytes(8) <= kLdsBytes && lds_bytes(2) <= kLdsBytes, "LDS of a block");
+constexpr int scale_bytes(int ts) { return (tile_rows(ts) + 2) * 16; }
+constexpr int scale_at(int ts) { return kAStages * a_bytes(ts) + b_stages(ts) * kBBytes; }
+constexpr int lds_bytes(int ts) { return scale_at(ts) + 2 * scale_bytes(ts); }
+constexpr int kLdsBytes = lds_bytes(7);
+static_assert(lds_bytes(4) <= kLdsBytes && lds_bytes(2) <= kLdsBytes, "LDS of a block");
 
-// Waits until at most N of this wave's loads are in flight, then for every
-// wave: their slices have arrived, and LDS reads before here have returned.
+// The end of a phase: this wave's LDS reads have returned and at most N of its
+// loads are in flight; then the same holds for every wave.
 template <int N>
-__device__ __forceinline__ void wait_loads()
+__device__ __forceinline__ void phase_end()
 {
+    __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
-// Every wave's LDS reads before here have returned.
-__device__ __forceinline__ void wait_reads()
+__device__ __forceinline__ void phase_end()
 {
+    __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // 16 bytes a lane straight to LDS: lane i's to dst + 16 * i. NT: stream. In
@@ -97,19 +105,29 @@ __device__ __forceinline__ void wait_reads()
 // so, the only waits are this file's own. No register is written, so nothing
 // the load does later can meet the compiler's registers, and its own counted
 // waits only get stricter by loads it does not know of.
-// dst is an LDS address. M0 holds it; nothing else here uses M0.
+// dst is an LDS address. M0 holds it; nothing else here uses M0. off is
+// checked against the resource; the column soff moves the address alone.
 template <bool NT>
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off)
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off, uint32_t soff)
 {
-    const int at = uniform((int)dst);
     if constexpr (NT)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
-                     ::"s"(at), "v"(off), "s"(rsrc)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                     ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
                      : "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     ::"s"(at), "v"(off), "s"(rsrc)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
                      : "memory");
+}
+
+// The same for lanes 0 to 31 alone. Every lane of the wave is active here.
+__device__ __forceinline__ void load_half_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off,
+                                                 uint32_t soff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, 0xffffffff\n\t"
+                 "buffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_mov_b64 exec, -1"
+                 ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
+                 : "memory");
 }
 
 // A base that every lane holds alike, and its row_rsrc, in scalar registers: a
@@ -128,7 +146,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base,
     return row_rsrc(uniform_ptr(base), (uint32_t)uniform((int)bytes));
 }
 
-// The same resource as its four words.
+// The same resource as its four words, and back.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(u32x4 w)
+{
+    const uint32_t lo = w[0], hi = w[1];
+    return row_rsrc(reinterpret_cast<const void*>(lo | (uint64_t)hi << 32), w[2]);
+}
+
 __device__ __forceinline__ u32x4 rsrc_words(const uint8_t* base, int bytes)
 {
     const uint64_t p = reinterpret_cast<uint64_t>(base);
@@ -164,32 +188,47 @@ __device__ __forceinline__ Widened widened(const i32x8& o)
     return r;
 }
 
+// Two fp16 values of an operand of 8, pair i of operand h, from the half of the
+// chunks that holds it.
+__device__ __forceinline__ uint32_t widened2(const i32x4& half, int h, int i)
+{
+    const int word = half[(h & 1) * 2 + (i >> 1)];
+    const f16x2 r = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, false);
+    return __builtin_bit_cast(uint32_t, r);
+}
+
 // One tile: the group's first row, how many rows, and the column tile.
 struct Tile {
     int64_t row0;   // first row (of [groups * cap])
     int group;
-    int rows;       // rows of the tile that exist, 1 .. 256; 0: no tile
+    int rows;       // rows of the tile that exist, 1 .. kTileRows; 0: no tile
     int col;        // column tile
 };
 
 // The loads of a tile's slices and scales. Wave w's i-th 1 KB of a slice holds
-// rows 8 * (8 * i + w) .. + 7, a lane one 16-byte chunk of a row.
+// rows 8 * (8 * i + w) .. + 7, a lane one 16-byte chunk of a row; the last 32
+// of 224 rows are shared by half waves, 4 rows each. Slices past the last are
+// asked for too, from beyond the resource's end (zeros, without memory
+// traffic), so that a step has the same loads in flight near the end and no
+// branch.
 // kSwiglu: weight rows [0, 128) of the tile are gate rows 128 * col .., rows
 // [128, 256) the up rows. Otherwise they are rows 256 * col .. .
 template <int TS, bool kSwiglu>
 struct Loads {
-    static constexpr int S = stages(TS);
+    static constexpr int SB = b_stages(TS);
     static constexpr int kRows = tile_rows(TS);
-    static constexpr int kALoads = kRows / 64;
-    static constexpr int kB = S * a_bytes(TS);              // offsets in LDS
-    static constexpr int kScale = kB + S * kBBytes;
+    static constexpr int kALoads = (kRows + 63) / 64;       // loads a wave and slice of rows
+    static constexpr int kAll = kALoads + kBLoads;          // and of both
+    static constexpr int kB = kAStages * a_bytes(TS);       // offsets in LDS
+    static constexpr int kScale = scale_at(TS);
     // weights of few rows are read once a call, and stream
-    static constexpr bool kBStream = TS < 8;
+    static constexpr bool kBStream = TS < kMaxTS;
 
-    const uint8_t *abase, *bbase, *sbase;   // uniform, as the sizes
-    int64_t bhalf;                           // from the tile's weight row 128 to row 0
-    int abytes, bbytes0, bbytes1, sbytes;
-    uint32_t aoff, boff, soff;
+    u32x4 ra, rb0, rb1, rs;                  // rows, the two halves of the weights, scales
+    int slanes;                              // lanes that load a scale
+    uint32_t aoff, alast, boff, soff;
+    uint32_t step64;                         // bytes of 64 rows of k
     int wave, nk;
     uint8_t* lds;                            // the block's, and its LDS address
     uint32_t lds0;
@@ -204,35 +243,38 @@ struct Loads {
         const uint32_t K = (uint32_t)a.k;
         const int lr = wave * 8 + (lane >> 3);      // row of i = 0; i adds 64
         const int chunk = lane & 7;
-        abase = uniform_ptr(a.a + t.row0 * K);
-        abytes = uniform(t.rows * (int)K);
+        step64 = 64 * K;
+        ra = rsrc_words(a.a + t.row0 * K, t.rows * (int)K);
         aoff = (uint32_t)lr * K + (uint32_t)((chunk ^ (lr & 7)) * 16);
+        const int hr = (kALoads - 1) * 64 + wave * 4 + (lane >> 3);
+        alast = kRows % 64 ? (uint32_t)hr * K + (uint32_t)((chunk ^ (hr & 7)) * 16)
+                           : aoff + (uint32_t)(kALoads - 1) * step64;
         // the key of a weight row: the bits in which the rows of an operand differ
-        constexpr int kKeyShift = kSwiglu ? 3 : 4;
-        const int key = (lr & 3) | (((lr >> kKeyShift) & 1) << 2);
+        const int key = (lr & 3) | (((lr >> 3) & 1) << 2);
         boff = (uint32_t)lr * K + (uint32_t)((chunk ^ key) * 16);
         const int64_t first = (int64_t)t.group * a.n;
         const int r0 = t.col * (kSwiglu ? 128 : kTileN);
         const int r1 = kSwiglu ? a.n / 2 + r0 : r0 + 128;
-        bbase = uniform_ptr(a.b + (first + r0) * K);
-        bhalf = (int64_t)(r1 - r0) * K;
-        bbytes0 = uniform(min(128, a.n - r0) * (int)K);
-        bbytes1 = uniform(max(0, min(128, a.n - r1)) * (int)K);
-        // wave w loads the scales of rows 64 w .., the wave after the last of
-        // them the two weight blocks' (lanes 0 and 1)
+        rb0 = rsrc_words(a.b + (first + r0) * K, min(128, a.n - r0) * (int)K);
+        rb1 = rsrc_words(a.b + (first + (r1 < a.n ? r1 : r0)) * K,
+                         max(0, min(128, a.n - r1)) * (int)K);
+        // wave w loads the scales of rows 64 w .. (below kRows), the wave after
+        // the last of them the two weight blocks' (lanes 0 and 1)
         const uint32_t srow = (uint32_t)nk * 4u;
-        if (wave < kRows / 64) {
-            sbase = uniform_ptr(a.as + (t.row0 + wave * 64) * srow);
-            sbytes = uniform(max(0, min(64, t.rows - wave * 64)) * (int)srow);
+        if (wave < kALoads) {
+            rs = rsrc_words(a.as + (t.row0 + wave * 64) * srow,
+                            max(0, min(64, t.rows - wave * 64)) * (int)srow);
             soff = (uint32_t)lane * srow;
+            slanes = uniform(min(64, kRows - wave * 64));
         } else {
             const int nb = (a.n + 127) / 128;
             const int b0 = kSwiglu ? t.col : t.col * 2;
             const int b1 = kSwiglu ? nb / 2 + t.col : min(b0 + 1, nb - 1);
             const int64_t block = (int64_t)t.group * nb + b0;
-            sbase = uniform_ptr(reinterpret_cast<const uint8_t*>(a.bs) + block * srow);
-            sbytes = uniform((b1 - b0 + 1) * (int)srow);
-            soff = (uint32_t)(lane == 0 ? 0 : lane == 1 ? b1 - b0 : b1 - b0 + 1) * srow;
+            rs = rsrc_words(reinterpret_cast<const uint8_t*>(a.bs) + block * srow,
+                            (b1 - b0 + 1) * (int)srow);
+            soff = (uint32_t)(lane == 1 ? b1 - b0 : 0) * srow;
+            slanes = uniform(wave == kALoads ? 2 : 0);
         }
     }
 
@@ -243,81 +285,93 @@ struct Loads {
         return min(kb & ~3, max(0, nk - 4));
     }
 
-    __device__ __forceinline__ void rows(int kb, int stage) const
+    // The scales of 4 steps, with the first of them.
+    __device__ __forceinline__ void scales(int kb) const
     {
-        if ((kb & 3) == 0 && wave <= kRows / 64) {
-            const uint32_t at = kScale + ((kb >> 2) & 1) * scale_bytes(TS) + wave * 1024;
+        const int lane = threadIdx.x & (kWave - 1);
+        if (kb < nk && (kb & 3) == 0 && lane < slanes) {
+            const int first = wave < kALoads ? wave * 64 : kRows;
+            const uint32_t at = kScale + ((kb >> 2) & 1) * scale_bytes(TS) + first * 16;
             if (nk >= 4) {
-                load_to_lds<false>(rsrc_words(sbase, sbytes), lds0 + at,
-                                   soff + (uint32_t)scale_start(kb) * 4u);
+                load_to_lds<false>(rs, lds0 + at, soff, (uint32_t)scale_start(kb) * 4u);
             } else {  // rows of 1 to 3 scales, once a tile
-                const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(sbase, sbytes);
-                float* own = reinterpret_cast<float*>(lds + at) + (threadIdx.x & (kWave - 1)) * 4;
+                const __amdgpu_buffer_rsrc_t r = rsrc_of(rs);
+                float* own = reinterpret_cast<float*>(lds + at) + lane * 4;
                 for (int c = 0; c < nk; ++c)
                     own[c] = __builtin_bit_cast(
-                        float, __builtin_amdgcn_raw_buffer_load_b32(rs, (int)soff, c * 4, 0));
+                        float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)soff, c * 4, 0));
             }
         }
-#pragma unroll
-        for (int i = 0; i < kALoads; ++i)
-            load_to_lds<false>(part(abase, abytes, i, kb),
-                               lds0 + stage * a_bytes(TS) + (i * 8 + wave) * 1024, aoff);
     }
 
-    __device__ __forceinline__ void weights(int kb, int stage) const
+    // Offset that takes a load of a slice past the last beyond any resource.
+    __device__ __forceinline__ uint32_t past(int kb) const { return kb < nk ? 0u : 1u << 30; }
+
+    // Load i of slice kb of the rows, or of the weights, to its stage.
+    __device__ __forceinline__ void row_load(int i, int kb, int stage) const
     {
-#pragma unroll
-        for (int i = 0; i < kBLoads; ++i)
-            load_to_lds<kBStream>(i < 2 ? part(bbase, bbytes0, i, kb)
-                                        : part(bbase + bhalf, bbytes1, i - 2, kb),
-                                  lds0 + kB + stage * kBBytes + (i * 8 + wave) * 1024, boff);
+        const uint32_t dst = lds0 + stage * a_bytes(TS) + i * 8192;
+        if (kRows % 64 && i == kALoads - 1)
+            load_half_to_lds(ra, dst + wave * 512, alast + past(kb), (uint32_t)kb * kSlice);
+        else
+            load_to_lds<false>(ra, dst + wave * 1024, aoff + i * step64 + past(kb),
+                               (uint32_t)kb * kSlice);
     }
 
-    // The rows from the i-th 64 on, from column kb * 128 on: a row of the tile
-    // starts inside the bytes that are left and the first row past it does not.
-    __device__ __forceinline__ u32x4 part(const uint8_t* base, int bytes, int i, int kb) const
+    __device__ __forceinline__ void weight_load(int i, int kb, int stage) const
     {
-        const int skip = i * 64 * nk * kSlice + kb * kSlice;
-        return rsrc_words(base + skip, max(0, bytes - skip));
+        load_to_lds<kBStream>(i < 2 ? rb0 : rb1,
+                              lds0 + kB + stage * kBBytes + i * 8192 + wave * 1024,
+                              boff + (i & 1) * step64 + past(kb), (uint32_t)kb * kSlice);
     }
 
-    // The first slices, in the order in which the steps ask for them: the
-    // weights are one slice ahead of the rows.
+    // The first slices, in the order in which the steps ask for them.
     __device__ __forceinline__ void prologue() const
     {
-        weights(0, 0);
+        auto weights = [&](int kb) {
 #pragma unroll
-        for (int i = 0; i < S - 1; ++i) {
-            if (i < nk)
-                rows(i, i);
-            if (i + 1 < nk)
-                weights(i + 1, i + 1);
+            for (int i = 0; i < kBLoads; ++i)
+                weight_load(i, kb, kb);
+        };
+#pragma unroll
+        for (int kb = 0; kb < SB - 2; ++kb)
+            weights(kb);
+        scales(0);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+            for (int i = 0; i < kALoads; ++i)
+                row_load(i, kb, kb);
+            weights(SB - 2 + kb);
         }
     }
 };
 
-// The sums of one tile, whose first slices are on their way.
+// The sums of one tile, whose first slices are on their way. A step has two
+// barriers. The first waits for the step's slices and ends the reads of the
+// step before, so the place of the rows' slice kb - 1 is free for slice kb +
+// 2. Then every wave takes its weights' operands to registers; the second
+// barrier frees their place for slice kb + SB. The products follow, each
+// matrix instruction with as much other work as runs beside it, and the loads
+// spread among them: issued together they hold up the waves, which issue in
+// order, until the load unit has taken them.
 template <int TS, bool kSwiglu>
-__device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
-                                         f32x4 (&acc)[TS][kSubs])
+__device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, f32x4 (&acc)[TS][kSubs])
 {
     using L = Loads<TS, kSwiglu>;
-    constexpr int S = L::S;
+    constexpr int SB = L::SB;
     const uint8_t* lds = ld.lds;
     const int lane = threadIdx.x & (kWave - 1);
     const int wm = ld.wave >> 2, wn = ld.wave & 3;
     const int q = lane >> 4, i16 = lane & 15;
     // a lane's row of each operand, its chunks q and q + 4 (exclusive-or 4)
-    constexpr int kKeyShift = kSwiglu ? 3 : 4;
-    const int wrow = kSwiglu ? wn * 32 + 8 * (i16 >> 2) + (i16 & 3)
-                             : wn * kWaveRows + 16 * (i16 >> 2) + (i16 & 3);
-    const int wkey = (wrow & 3) | (((wrow >> kKeyShift) & 1) << 2);
+    const int wrow = wn * (kSwiglu ? 32 : kWaveRows) + 8 * (i16 >> 2) + (i16 & 3);
+    const int wkey = (wrow & 3) | (((wrow >> 3) & 1) << 2);
     const uint32_t wlo = L::kB + (uint32_t)wrow * kSlice + (uint32_t)((q ^ wkey) * 16);
     const int trow = wm * 16 * TS + i16;
     const uint32_t tlo = (uint32_t)trow * kSlice + (uint32_t)((q ^ (trow & 7)) * 16);
     auto sub_offset = [](int s) {
-        return kSwiglu ? (uint32_t)((s & 1) * 4 + (s >> 1) * 128) * kSlice
-                       : (uint32_t)(s * 4) * kSlice;
+        return (uint32_t)((s & 1) * 4 + (s >> 1) * (kSwiglu ? 128 : 32)) * kSlice;
     };
 
 #pragma unroll
@@ -327,47 +381,71 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
             acc[j][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const int nk = ld.nk;
-    int stage = 0;
+    // Loads a wave has in flight when a step starts, of those asked for after
+    // the step's rows (with two stages its weights come after them). Scales
+    // come on top now and then, which only makes the wait stricter.
+    constexpr int kLater = SB > 2 ? L::kAll + kBLoads : L::kAll;
+
+    int sta = 0, stb = 0;  // stages of step kb
     for (int kb = 0; kb < nk; ++kb) {
-        // Issued after this step's rows: S - 1 slices of weights and S - 2 of
-        // rows, fewer near the end.
-        if (kb + S <= nk)
-            wait_loads<(S - 1) * kBLoads + (S - 2) * L::kALoads>();
-        else
-            wait_loads<0>();
-        const uint8_t* sa = lds + stage * a_bytes(TS);
-        const uint8_t* sb = lds + stage * kBBytes;
-        auto weights = [&](int s) {
-            return operand(sb + wlo + sub_offset(s), sb + (wlo ^ 64) + sub_offset(s));
+        const uint8_t* sa = lds + sta * a_bytes(TS);
+        const uint8_t* sb = lds + stb * kBBytes;
+        static_assert(kAStages == 3, "stage of step kb + 2");
+        // 16 bytes of this lane's row of operand j: chunk q (half 0) or q + 4
+        auto tokens = [&](int j, int half) {
+            return *reinterpret_cast<const i32x4*>(sa + (half ? tlo ^ 64 : tlo) + j * 16 * kSlice);
         };
-        auto tokens = [&](int j) {
-            return operand(sa + tlo + j * 16 * kSlice, sa + (tlo ^ 64) + j * 16 * kSlice);
+        phase_end<kLater>();
+        ld.scales(kb + 2);
+        const int free_a = sta == 0 ? 2 : sta - 1;
+        // load `i` of the step's, rows first
+        auto ask = [&](int i) {
+            if (i < L::kALoads)
+                ld.row_load(i, kb + 2, free_a);
+            else
+                ld.weight_load(i - L::kALoads, kb + SB, stb);
         };
-        if (kb + S - 1 < nk)
-            ld.rows(kb + S - 1, stage == 0 ? S - 1 : stage - 1);
         i32x8 w[kSubs];
 #pragma unroll
         for (int s = 0; s < kSubs; ++s)
-            w[s] = weights(s);
-        const float* scale = reinterpret_cast<const float*>(
-                                 lds + L::kScale + ((kb >> 2) & 1) * scale_bytes(TS)) +
-                             (kb - ld.scale_start(kb));
+            w[s] = operand(sb + wlo + sub_offset(s), sb + (wlo ^ 64) + sub_offset(s));
+        const float* scale =
+            reinterpret_cast<const float*>(lds + L::kScale + ((kb >> 2) & 1) * scale_bytes(TS)) +
+            (kb - ld.scale_start(kb));
         const float wb0 = scale[(L::kRows + (kSwiglu ? 0 : wn >> 1)) * 4];
         const float wb1 = kSwiglu ? scale[(L::kRows + 1) * 4] : wb0;
-        i32x8 x = tokens(0);
-        // the weights' slice is in registers: its place takes the next but S - 1
-        wait_reads();
-        if (kb + S < nk)
-            ld.weights(kb + S, stage);
+        float sx = scale[trow * 4];
+        i32x4 lo = tokens(0, 0), hi = tokens(0, 1);
+        phase_end();
+        Widened v[kSwiglu ? kSubs : 1];
+        u32x4 y[2];  // operands of 8 values, in turn
+        if constexpr (kSwiglu) {
+#pragma unroll
+            for (int s = 0; s < kSubs; ++s)
+                v[s] = widened(w[s]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[0][i] = widened2(lo, 0, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        auto asks = [&](int j) {  // the loads of operand j's turn
+#pragma unroll
+            for (int i = 0; i < L::kAll; ++i)
+                if (i * TS / L::kAll == j)
+                    ask(i);
+        };
+        f32x4 old[kSubs];  // the products of operand j - 1
+        float oldc0 = 0.0f, oldc1 = 0.0f;
         if constexpr (!kSwiglu) {
-            f32x4 old[kSubs];
-            float oldc = 0.0f;
 #pragma unroll
             for (int j = 0; j < TS; ++j) {
-                i32x8 next = x;
-                if (j + 1 < TS)
-                    next = tokens(j + 1);
-                const float c = scale[(trow + j * 16) * 4] * wb0;
+                const i32x8 x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                const float c = sx * wb0;
+                if (j + 1 < TS) {
+                    lo = tokens(j + 1, 0);
+                    hi = tokens(j + 1, 1);
+                    sx = scale[(trow + (j + 1) * 16) * 4];
+                }
                 f32x4 p[kSubs];
 #pragma unroll
                 for (int s = 0; s < kSubs; ++s) {
@@ -376,60 +454,73 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
                     if (j > 0) {
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            acc[j - 1][s][r] = __builtin_fmaf(old[s][r], oldc, acc[j - 1][s][r]);
+                            acc[j - 1][s][r] = __builtin_fmaf(old[s][r], oldc0, acc[j - 1][s][r]);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                asks(j);
+#pragma unroll
+                for (int s = 0; s < kSubs; ++s)
+                    old[s] = p[s];
+                oldc0 = c;
+            }
+            oldc1 = oldc0;
+        } else {
+#pragma unroll
+            for (int j = 0; j < TS; ++j) {
+                const float c0 = sx * wb0, c1 = sx * wb1;
+                f32x4 p[kSubs];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                    for (int s = 0; s < kSubs; ++s) {
+                        p[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            v[s].v[h], __builtin_bit_cast(f16x8, y[h & 1]),
+                            h == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p[s], 0, 0, 0);
+                        // one value pair of the next operand
+                        if (h < 3)
+                            y[(h + 1) & 1][s] = widened2(h == 0 ? lo : hi, h + 1, s);
+                        else if (j + 1 < TS)
+                            y[0][s] = widened2(lo, 0, s);
+                        // and one sum of the products before
+                        if (j > 0)
+                            acc[j - 1][h][s] =
+                                __builtin_fmaf(old[h][s], h < 2 ? oldc0 : oldc1, acc[j - 1][h][s]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if (j + 1 < TS) {  // the halves are read again as soon as they are widened
+                        if (h == 0)
+                            lo = tokens(j + 1, 0);
+                        if (h == 2)
+                            hi = tokens(j + 1, 1);
+                        if (h == 3)
+                            sx = scale[(trow + (j + 1) * 16) * 4];
+                    }
+                    if (h == 1)
+                        asks(j);
                 }
 #pragma unroll
                 for (int s = 0; s < kSubs; ++s)
                     old[s] = p[s];
-                oldc = c;
-                x = next;
-            }
-#pragma unroll
-            for (int s = 0; s < kSubs; ++s)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    acc[TS - 1][s][r] = __builtin_fmaf(old[s][r], oldc, acc[TS - 1][s][r]);
-        } else {
-            Widened v[kSubs];
-#pragma unroll
-            for (int s = 0; s < kSubs; ++s)
-                v[s] = widened(w[s]);
-#pragma unroll
-            for (int j = 0; j < TS; ++j) {
-                const Widened y = widened(x);
-                if (j + 1 < TS)
-                    x = tokens(j + 1);
-                const float sx = scale[(trow + j * 16) * 4];
-                const float c0 = sx * wb0, c1 = sx * wb1;
-#pragma unroll
-                for (int s0 = 0; s0 < kSubs; s0 += 2) {
-                    f32x4 p[2];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-                            p[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                                v[s0 + s].v[h], y.v[h],
-                                h == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p[s], 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            acc[j][s0 + s][r] =
-                                __builtin_fmaf(p[s][r], s0 ? c1 : c0, acc[j][s0 + s][r]);
-                    }
-                }
+                oldc0 = c0;
+                oldc1 = c1;
             }
         }
-        stage = stage + 1 == S ? 0 : stage + 1;
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc[TS - 1][s][r] =
+                    __builtin_fmaf(old[s][r], s < 2 ? oldc0 : oldc1, acc[TS - 1][s][r]);
+        sta = sta == 2 ? 0 : sta + 1;
+        stb = stb + 1 == SB ? 0 : stb + 1;
     }
+    phase_end();
 }
 
 // The tile's sums to memory.
 template <int TS, int DT, bool kSwiglu>
-__device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (*s_amax)[256],
+__device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (*s_amax)[tile_rows(TS)],
                                        f32x4 (&acc)[TS][kSubs])
 {
     const int lane = threadIdx.x & (kWave - 1);
@@ -439,8 +530,9 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
     const int trow0 = wm * 16 * TS + (lane & 15);
     // ---- epilogue
     if constexpr (!kSwiglu) {
-        // a lane holds 16 consecutive columns of each of its rows
-        const int col = t.col * kTileN + wn * kWaveRows + q * 16;
+        // a lane holds two runs of 8 columns of each of its rows; the 4 lanes of
+        // a row write 64 bytes together
+        const int col = t.col * kTileN + wn * kWaveRows + q * 8;
         const __amdgpu_buffer_rsrc_t ro =
             uniform_rsrc(a.out + t.row0 * a.n * 2, (uint32_t)t.rows * (uint32_t)a.n * 2u);
 #pragma unroll
@@ -454,8 +546,8 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
                     f[r] = acc[j][2 * h][r];
                     f[4 + r] = acc[j][2 * h + 1][r];
                 }
-                if (col + h * 8 < a.n)  // rows past the tile's are dropped by the resource
-                    bstore16<0>(narrow<DT>(f), ro, at + h * 16u);
+                if (col + h * 32 < a.n)  // rows past the tile's are dropped by the resource
+                    bstore16<0>(narrow<DT>(f), ro, at + h * 64u);
             }
         }
     } else {
@@ -480,7 +572,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
             if (q == 0)
                 s_amax[wn][trow0 + j * 16] = amax;
         }
-        __syncthreads();
+        phase_end();
         const int inter = a.n / 2;
         const int col = t.col * 128 + wn * 32 + q * 8;
         const __amdgpu_buffer_rsrc_t ro =
@@ -508,14 +600,13 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
 }
 
 // Operands of 16 rows a wave that a tile of this many rows needs.
-__device__ __forceinline__ int tile_class(int rows) { return rows > 128 ? 8 : rows > 64 ? 4 : 2; }
+__device__ __forceinline__ int tile_class(int rows) { return rows > 128 ? 7 : rows > 64 ? 4 : 2; }
 
 template <int DT, bool kSwiglu>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 moe_gemm_kernel(GemmArgs a)
 {
     __shared__ __align__(1024) uint8_t lds[kLdsBytes];
-    __shared__ float s_amax[4][256];
     __shared__ int s_part[kThreads / kWave];
     __shared__ int s_first[kThreads + 1];
     __shared__ int s_tile[2][4];
@@ -534,7 +625,7 @@ moe_gemm_kernel(GemmArgs a)
         const int g0 = min(a.groups, (int)threadIdx.x * share), g1 = min(a.groups, g0 + share);
         int mine = 0;
         for (int g = g0; g < g1; ++g)
-            mine += (rows_of(g) + 255) / 256;
+            mine += (rows_of(g) + kTileRows - 1) / kTileRows;
         int inc = mine;
 #pragma unroll
         for (int o = 1; o < kWave; o <<= 1) {
@@ -577,12 +668,12 @@ moe_gemm_kernel(GemmArgs a)
         int base = s_first[threadIdx.x];
         if (u < base || u >= s_first[threadIdx.x + 1])
             return;
-        int g = (int)threadIdx.x * share, rows = rows_of(g), n = (rows + 255) / 256;
+        int g = (int)threadIdx.x * share, rows = rows_of(g), n = (rows + kTileRows - 1) / kTileRows;
         while (u >= base + n) {
             base += n;
             ++g;
             rows = rows_of(g);
-            n = (rows + 255) / 256;
+            n = (rows + kTileRows - 1) / kTileRows;
         }
         const int at = (int)(tile - (int64_t)base * a.col_tiles);
         info[0] = g;
@@ -594,9 +685,9 @@ moe_gemm_kernel(GemmArgs a)
         Tile t;
         t.group = uniform(info[0]);
         const int m = uniform(info[2]);
-        t.rows = min(256, uniform(info[1]) - m * 256);
+        t.rows = min(kTileRows, uniform(info[1]) - m * kTileRows);
         t.col = uniform(info[3]);
-        t.row0 = (int64_t)t.group * a.cap + m * 256;
+        t.row0 = (int64_t)t.group * a.cap + m * kTileRows;
         return t;
     };
 
@@ -613,8 +704,12 @@ moe_gemm_kernel(GemmArgs a)
     auto run = [&](auto ts) {
         constexpr int TS = decltype(ts)::value;
         const Loads<TS, kSwiglu> ld(a, t, lds, lds0);
-        if (!loading)
+        if (!loading) {
+            // a tile of another class may still use its block maxima, and its
+            // loads past the end may still write
+            phase_end<0>();
             ld.prologue();
+        }
         t0 += gridDim.x;
         const int64_t next = tile_at(t0);
         slot ^= 1;
@@ -622,7 +717,6 @@ moe_gemm_kernel(GemmArgs a)
             look_up(next, s_tile[slot]);  // read after the steps' barriers
         f32x4 acc[TS][kSubs];
         multiply<TS, kSwiglu>(ld, acc);
-        wait_reads();
         const Tile done = t;
         t.rows = 0;
         loading = false;
@@ -635,15 +729,21 @@ moe_gemm_kernel(GemmArgs a)
                 loading = true;
             }
         }
-        finish<TS, DT, kSwiglu>(a, done, s_amax, acc);
+        // the block maxima go where the second block of scales was: the next
+        // tile asks for that one after its first phases
+        static_assert(scale_bytes(TS) >= (int)sizeof(float) * 4 * tile_rows(TS), "block maxima");
+        finish<TS, DT, kSwiglu>(
+            a, done,
+            reinterpret_cast<float(*)[tile_rows(TS)]>(lds + scale_at(TS) + scale_bytes(TS)), acc);
     };
     while (t.rows > 0) {
         switch (tile_class(t.rows)) {
-        case 8: run(std::integral_constant<int, 8>()); break;
+        case 7: run(std::integral_constant<int, 7>()); break;
         case 4: run(std::integral_constant<int, 4>()); break;
         default: run(std::integral_constant<int, 2>()); break;
         }
     }
+    phase_end<0>();  // no load may write LDS after the block's end
 }
 
 }  // namespace
