@@ -87,13 +87,17 @@ def _refuse(t, name, shape, dtypes, index):
 
 def _ptr(t: Optional[torch.Tensor], name: str, shape, dtypes, index: int):
     """Address of a contiguous tensor of exactly this shape, one of these
-    element types and on device `index`; None stays None."""
+    element types and on device `index` (CPU tensors are on -1); None stays
+    None."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == index and
-            t.shape == shape and t.dtype in dtypes and t.is_contiguous()):
-        _refuse(t, name, shape, dtypes, index)
-    return t.data_ptr()
+    try:
+        if (t.get_device() == index and t.shape == shape and t.dtype in dtypes and
+                t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, dtypes, index)
 
 
 def _index_of(t, name: str) -> int:
