@@ -842,21 +842,22 @@ class EpDispatchCombineOp:
             raise ValueError(f"gate_up and down must be {[G, 2 * inter, H]} and {[G, H, inter]}, "
                              f"not {list(gate_up.shape)} and {list(down.shape)}")
         ex = self._expert_state()
-        if ex.get("inter") != inter:
+        # buffers of each hidden size are kept until close(): a captured graph
+        # may hold them
+        bufs = ex.setdefault("mlp", {})
+        if inter not in bufs:
             dev = self.workspace.device
-            ex["hidden"] = torch.empty((G, cap, inter), dtype=torch.uint8, device=dev)
-            ex["hidden_scales"] = torch.empty((G, cap, inter // 128), dtype=torch.float32,
-                                              device=dev)
-            ex["mlp_y"] = torch.empty((W, Er, cap, H), dtype=_TORCH[cfg.combine_dtype],
-                                      device=dev)
-            ex["inter"] = inter
+            bufs[inter] = (torch.empty((G, cap, inter), dtype=torch.uint8, device=dev),
+                           torch.empty((G, cap, inter // 128), dtype=torch.float32, device=dev),
+                           torch.empty((W, Er, cap, H), dtype=_TORCH[cfg.combine_dtype],
+                                       device=dev))
+        hidden, hidden_scales, y = bufs[inter]
         counts = packed_recv_count.view(G)
         moe_grouped_gemm_swiglu(rows.view(G, cap, H), scales.view(torch.float32).view(
-            G, cap, H // 128), gate_up, gate_up_scales, ex["hidden"], ex["hidden_scales"], counts,
-            stream)
-        moe_grouped_gemm(ex["hidden"], ex["hidden_scales"], down, down_scales,
-                         ex["mlp_y"].view(G, cap, H), counts, stream)
-        return ex["mlp_y"]
+            G, cap, H // 128), gate_up, gate_up_scales, hidden, hidden_scales, counts, stream)
+        moe_grouped_gemm(hidden, hidden_scales, down, down_scales, y.view(G, cap, H), counts,
+                         stream)
+        return y
 
     def combine_standard_moe_backward(self, grad_out, weights, indices, packed_y=None,
                                       grad_packed_y=None, grad_weights=None, stream=None):

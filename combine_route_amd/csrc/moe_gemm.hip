@@ -564,8 +564,10 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float g = acc[j][s][r];
-                    const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
-                    const float z = g * sig * acc[j][2 + s][r];
+                    // both sides of the quotient over 16, so that the reciprocal
+                    // stays in the normal range wherever the exponential is finite
+                    const float d = __builtin_fmaf(__expf(-g), 0.0625f, 0.0625f);
+                    const float z = g * 0.0625f * __builtin_amdgcn_rcpf(d) * acc[j][2 + s][r];
                     acc[j][s][r] = z;
                     amax = __builtin_fmaxf(amax, __builtin_fabsf(z));
                 }

@@ -171,8 +171,9 @@ int moe_grouped_gemm(const moe_grouped_gemm_args_t* a, void* stream_ptr)
     const int step = swiglu ? 256 : 8;
     if (a->n < step || a->n % step)
         return fail(EP_ERR_ARG, "args.n = %d: must be a positive multiple of %d", a->n, step);
-    if (a->n > (1 << 20) || a->k > (1 << 20))
-        return fail(EP_ERR_SIZE, "args.n = %d, args.k = %d: must be at most 2^20", a->n, a->k);
+    if (a->n > (1 << 20) || a->k > (1 << 20) || a->groups > (1 << 20))
+        return fail(EP_ERR_SIZE, "args.n = %d, args.k = %d, args.groups = %d: must be at most "
+                    "2^20", a->n, a->k, a->groups);
     if ((int64_t)a->groups * a->cap > INT32_MAX)
         return fail(EP_ERR_SIZE, "args.groups * args.cap = %lld exceeds 2^31 - 1",
                     (long long)a->groups * a->cap);

@@ -114,6 +114,8 @@ def _call(fn, index, stream, *args):
     or torch's current one there."""
     if not _fns:
         _lib()
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     if torch.cuda.current_device() == index:
         rc = _fns[fn](*args, _stream(stream, index))
     else:

@@ -185,6 +185,79 @@ def test_special_values_stay_in_their_rows():
     assert torch.equal(got[rest], want[rest])
 
 
+def test_every_code_is_taken_as_its_value():
+    """Row r has code r once, against a weight of one: the output is the
+    code's value (4 significant bits: exact in bf16), subnormals and NaN among
+    them."""
+    a = torch.zeros((1, 256, 128), dtype=torch.uint8)
+    a[0, :, 37] = torch.arange(256)
+    b = torch.zeros((1, 512, 128))
+    b[0, :, 37] = 1.0
+    one = torch.ones((1, 256, 1)), b.to(ref.E4M3), torch.ones((1, 4, 1))
+    out = run_rows((a.view(ref.E4M3),) + one, None, torch.bfloat16).cpu()
+    want = torch.arange(256, dtype=torch.uint8).view(ref.E4M3).float()
+    nan = want.isnan()
+    assert int(nan.sum()) == 2 and bool(out[0][nan].isnan().all())
+    assert torch.equal(out[0][~nan].float(), want[~nan, None].expand(-1, 512))
+    codes, scales = (v.cpu() for v in run_swiglu((a.view(ref.E4M3),) + one, None))
+    assert bool((codes[0][nan] == 0x7F).all()) and bool((scales[0][nan] == 1).all())
+    v = want[~nan].double()[:, None].expand(-1, 256)
+    # exp(-gate) is infinite in FP32 below -88.7, and the quotient 0
+    z = torch.where(v < -88.7, 0.0, v * torch.sigmoid(v) * v)
+    ref.quantized_close(codes[0][~nan], scales[0][~nan], z, 0.0, (8 + v.abs()) * ref.F32 * z.abs())
+
+
+def test_special_values_stay_in_their_rows_swiglu():
+    a, sa, b, sb = inputs(2, 70, 512, 384, seed=7)
+    wc, ws = run_swiglu((a, sa, b, sb), None)
+    a.view(torch.uint8)[0, 3, 100] = 0x7F
+    sa[1, 65, 2] = float("nan")
+    sa[1, 2, 0] = float("inf")
+    c, s = run_swiglu((a, sa, b, sb), None)
+    assert bool((c[0, 3] == 0x7F).all()) and bool((c[1, 65] == 0x7F).all())
+    keep = torch.ones(2, 70, dtype=torch.bool)
+    keep[0, 3] = keep[1, 65] = keep[1, 2] = False
+    assert torch.equal(c[keep], wc[keep]) and torch.equal(s[keep], ws[keep])
+
+
+@pytest.mark.parametrize("k", [128, 256, 384, 512, 640, 768, 896, 1152])
+def test_step_counts(k):
+    """Few steps, and every remainder of the four steps whose scales are read
+    together, in each size of tile."""
+    inp = inputs(4, 230, 512, k, seed=k)
+    counts = [230, 225, 100, 40]
+    out = run_rows(inp, device_counts(counts), torch.bfloat16).cpu()
+    codes, scales = (v.cpu() for v in run_swiglu(inp, device_counts(counts)))
+    y, size = product(*inp)
+    z, err = swiglu(y, size, k)
+    for g, c in enumerate(counts):
+        ref.close_to(out[g, :c], y[g, :c], torch.bfloat16, 0.0, (CUT + slack(k)) * size[g, :c])
+        off = (out[g, :c].double() - y[g, :c]).norm()
+        assert float(off) <= ref.half_step(torch.bfloat16) * float(y[g, :c].norm())
+        ref.quantized_close(codes[g, :c], scales[g, :c], z[g, :c], 0.0, err[g, :c])
+
+
+def test_many_tiles_a_block():
+    """More tiles than blocks, of every size, so that blocks go from one size
+    to another with loads in flight."""
+    g = torch.Generator().manual_seed(3)
+    G, cap, n, k = 64, 300, 2048, 256
+    counts = torch.randint(0, cap + 20, (G,), generator=g).tolist()
+    inp = inputs(G, cap, n, k, seed=9)
+    out = run_rows(inp, device_counts(counts), torch.bfloat16)
+    codes, scales = run_swiglu(inp, device_counts(counts))
+    for e in range(0, G, 7):
+        c = min(cap, counts[e])
+        one = tuple(v[e:e + 1] for v in inp)
+        y, size = product(*one)
+        ref.close_to(out[e, :c].cpu(), y[0, :c], torch.bfloat16, 0.0,
+                     (CUT + slack(k)) * size[0, :c])
+        z, err = swiglu(y, size, k)
+        if c:
+            ref.quantized_close(codes[e, :c].cpu(), scales[e, :c].cpu(), z[0, :c], 0.0, err[0, :c])
+        assert bool((out[e, c:] == 7).all()) and bool((codes[e, c:] == 77).all())
+
+
 def test_rows_past_the_count_are_not_read():
     inp = inputs(2, 300, 256, 256, seed=3)
     counts = device_counts([130, 7])

@@ -178,6 +178,7 @@ BAD_GEMM = [
     (dict(n=(1 << 20) + 8), cra.EP_ERR_SIZE, "args.n"),
     (dict(k=(1 << 20) + 128), cra.EP_ERR_SIZE, "args.k"),
     (dict(groups=1 << 16, cap=1 << 16), cra.EP_ERR_SIZE, "groups"),
+    (dict(groups=(1 << 20) + 1, cap=1), cra.EP_ERR_SIZE, "groups"),
     (dict(out_dtype=cra.EP_FP8_E4M3), cra.EP_ERR_ARG, "out_dtype"),
     (dict(SWIGLU, out_dtype=cra.EP_BF16), cra.EP_ERR_ARG, "out_dtype"),
     (dict(epilogue=2), cra.EP_ERR_ARG, "epilogue"),
