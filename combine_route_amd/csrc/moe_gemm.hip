@@ -4,11 +4,11 @@
 // to bf16 / fp16 rows or, with gate and up weights, to FP8 rows of
 // silu(gate) * up with their own scales.
 //
-// A work item is a tile of up to 256 rows of one expert by 256 weight rows.
+// A work item is a tile of up to 224 rows of one expert by 256 weight rows.
 // Row counts are on the GPU, so the launch is a fixed grid of one block a
 // compute unit; each block works out every expert's tile range from the
 // counts and walks its share of the tiles. An expert's last tile computes as
-// few of 64, 128 or 256 rows as hold its rows, so that experts with few rows
+// few of 64, 128 or 224 rows as hold its rows, so that experts with few rows
 // cost their weights' bytes and little else.
 //
 // The FP8 matrix instruction adds 8 products at a time after aligning them to
@@ -17,23 +17,41 @@
 // across them; the same in v_mfma_f32_16x16x32_fp8_fp8). Rows of bf16 / fp16
 // take it: its error, 1.3e-5 of a row's norm whatever k, is 1/20 of fp16's
 // rounding and 1/150 of bf16's. The swiglu form returns its block scales in
-// FP32, so there both operands are widened to fp16 (exact) in registers and
-// multiplied by v_mfma_f32_16x16x32_f16, whose sums of such products are
-// FP32's; the matrix rate is half.
+// FP32 (off by 1.2e-5 that way), so there both operands are widened to fp16
+// (exact) in registers and multiplied by v_mfma_f32_16x16x32_f16, whose sums
+// of such products are FP32's (scales off by 2e-7); the matrix rate is half.
 //
 // Inside a tile: 8 waves, 2 along the rows x 4 along the weight rows. For
-// each 128 elements of k the block holds both operands' slices (128 bytes a
-// row) in LDS, loaded there directly from memory while the slices before are
-// multiplied. The matrix instruction is v_mfma_f32_16x16x128_f8f6f4 with the
-// weights as its rows and the token rows as its columns: one instruction
-// takes a whole scale block of k, and a lane then holds one token row's
-// partial sums, so the scales' product is one value a lane and the partial
-// joins the FP32 sum with a fused multiply-add an element.
+// each 128 elements of k (a step) the block holds both operands' slices (128
+// bytes a row) in LDS, loaded there directly from memory two steps and more
+// before. The matrix instruction has the weights as its rows and the token
+// rows as its columns: v_mfma_f32_16x16x128_f8f6f4 takes a whole scale block
+// of k, a lane then holds one token row's partial sums, so the scales'
+// product is one value a lane and the partial joins the FP32 sum with a fused
+// multiply-add an element, beside the next matrix instruction. 224 rows: the
+// largest tile whose rows' slices fit LDS three times beside two of the
+// weights' (256 rows with two of each: 1009 against 960 us at 32 experts x
+// 1024 rows, k 7168, n 4096).
 //
 // LDS slices are 128 bytes a row without padding; the eight 16-byte chunks of
 // a row are permuted by a key of the row, so the 16 rows a matrix operand
 // reads together fall in different banks. Both operands take the chunks in
 // the same order, so the order of k inside an instruction is the same too.
+//
+// Measured on MI355X (a large FP8 library product: 2.6 PFLOP/s, bf16 1.35;
+// weights streamed to LDS alone: 7.0 TB/s): 32 experts x 1024 rows, n 7168, k
+// 2048 545 us (1.77 PFLOP/s), n 4096, k 7168 960 us (2.0); gate and up, n
+// 4096, k 7168, 32768 rows in all 1.7 to 1.8 ms (1.1 PFLOP/s in fp16
+// products; without its loads 1.4 ms). Large tiles are bound by the matrix
+// units' power and the sums beside them: without their loads they take 780 us
+// instead of 960. 256 experts x 32 rows, n 7168, k 2048 680 us (5.7 TB/s; 545 without its
+// stores: 117 MB of scattered rows in a stream of reads), gate and up of 32
+// experts x 32 rows 182 us (5.2 TB/s): bound by memory. Tried and no faster:
+// the wave halves taking turns at reading and multiplying (1108 against 1010
+// us), raised wave priority, products of 32 x 32 x 16 in the swiglu form (2.0
+// ms: a product's 32 sums run in one piece), operands a step ahead in tiles of
+// few rows, streamed weights in large tiles (1027 against 972 us), one range
+// of tiles an XCD (790 against 745 us with skewed rows).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -105,8 +123,9 @@ __device__ __forceinline__ void phase_end()
 // so, the only waits are this file's own. No register is written, so nothing
 // the load does later can meet the compiler's registers, and its own counted
 // waits only get stricter by loads it does not know of.
-// dst is an LDS address. M0 holds it; nothing else here uses M0. off is
-// checked against the resource; the column soff moves the address alone.
+// dst is an LDS address. M0 holds it; nothing else here uses M0. What is
+// checked against the resource's bytes is off + soff, whichever part of it is
+// past them (measured on gfx950, soff past them too).
 template <bool NT>
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off, uint32_t soff)
 {
@@ -222,7 +241,8 @@ struct Loads {
     static constexpr int kAll = kALoads + kBLoads;          // and of both
     static constexpr int kB = kAStages * a_bytes(TS);       // offsets in LDS
     static constexpr int kScale = scale_at(TS);
-    // weights of few rows are read once a call, and stream
+    // weights of few rows are read once a call, and stream (a stream of
+    // weights alone reaches 7.0 TB/s so, 6.2 without)
     static constexpr bool kBStream = TS < kMaxTS;
 
     u32x4 ra, rb0, rb1, rs;                  // rows, the two halves of the weights, scales
@@ -533,7 +553,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
         // a lane holds two runs of 8 columns of each of its rows; the 4 lanes of
         // a row write 64 bytes together. Rows few and far between are written
         // through the L2 (sc1), which the weights stream through (256 experts x
-        // 32 rows, k 2048, n 7168: 716 -> 687 us).
+        // 32 rows, k 2048, n 7168: 716 -> 680 us).
         constexpr int kStore = TS < kMaxTS ? 16 : 0;
         const int col = t.col * kTileN + wn * kWaveRows + q * 8;
         const __amdgpu_buffer_rsrc_t ro =

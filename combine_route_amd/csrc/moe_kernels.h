@@ -64,8 +64,7 @@ struct DispatchBackwardArgs {
     const int32_t* fslot;        // [W][M][k]
     uint8_t* gx;                 // [W][M][H]
     int32_t row_vecs;
-    int32_t piece_vecs;          // vectors a wave sums: 64 or 128
-    int32_t pieces;
+    int32_t pieces;              // of 64 vectors, a wave each
     int32_t M, k;
 };
 
