@@ -868,7 +868,7 @@ class EpDispatchCombineOp:
         taken with weights. Rows of no kept pair and of tokens t >= T_r are
         left untouched. The results are the tensors given for them, or new
         ones (zeros)."""
-        ex = self._fused_state("combine_standard_moe_backward")
+        ex = self._fused_state("combine_standard_moe_backward", grad_out, "grad_out")
         cfg = self.cfg
         W, M, k = cfg.world_size, cfg.max_num_inp_token_per_rank, cfg.num_experts_per_token
         if grad_packed_y is None:
@@ -885,7 +885,7 @@ class EpDispatchCombineOp:
         grad_packed_x [W, Er, cap, H], both in the combine type. Rows of
         tokens t >= T_r are left untouched. Returns the tensor given for it,
         or a new one (zeros)."""
-        ex = self._fused_state("dispatch_standard_moe_backward")
+        ex = self._fused_state("dispatch_standard_moe_backward", grad_packed_x, "grad_packed_x")
         cfg = self.cfg
         if grad_x is None:
             grad_x = self._zeros((cfg.world_size, cfg.max_num_inp_token_per_rank, cfg.hidden_dim),
@@ -903,9 +903,13 @@ class EpDispatchCombineOp:
         with torch.cuda.stream(stream):
             return torch.zeros(shape, dtype=dtype, device=self.workspace.device)
 
-    def _fused_state(self, call):
+    def _fused_state(self, call, given, name):
+        """The expert plan's state for a call on tensors that lie with `given`:
+        the plan's map is on the op's own device."""
         if self._ex is None:
             raise EpError(call, EP_ERR_STATE, f"{call} before any dispatch_standard_moe")
+        if given.device != self.workspace.device:
+            raise ValueError(f"{name} is on {given.device}, the op on {self.workspace.device}")
         return self._ex
 
     def close(self):

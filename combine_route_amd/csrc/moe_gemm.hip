@@ -44,14 +44,15 @@
 // 4096, k 7168, 32768 rows in all 1.7 to 1.8 ms (1.1 PFLOP/s in fp16
 // products; without its loads 1.4 ms). Large tiles are bound by the matrix
 // units' power and the sums beside them: without their loads they take 780 us
-// instead of 960. 256 experts x 32 rows, n 7168, k 2048 680 us (5.7 TB/s; 545 without its
-// stores: 117 MB of scattered rows in a stream of reads), gate and up of 32
-// experts x 32 rows 182 us (5.2 TB/s): bound by memory. Tried and no faster:
-// the wave halves taking turns at reading and multiplying (1108 against 1010
-// us), raised wave priority, products of 32 x 32 x 16 in the swiglu form (2.0
-// ms: a product's 32 sums run in one piece), operands a step ahead in tiles of
-// few rows, streamed weights in large tiles (1027 against 972 us), one range
-// of tiles an XCD (790 against 745 us with skewed rows).
+// instead of 960. 256 experts x 32 rows, n 7168, k 2048 680 us (5.7 TB/s; 545
+// without its stores: 117 MB of scattered rows in a stream of reads), gate and
+// up of 32 experts x 32 rows 182 us (5.2 TB/s): bound by memory. Tried and no
+// faster: the wave halves taking turns at reading and multiplying (1108
+// against 1010 us), raised wave priority, a step's loads all in its first
+// products (980 against 950 us), products of 32 x 32 x 16 in the swiglu form
+// (2.0 ms: a product's 32 sums run in one piece), operands a step ahead in
+// tiles of few rows, streamed weights in large tiles (1027 against 972 us),
+// one range of tiles an XCD (790 against 745 us with skewed rows).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -66,7 +66,8 @@ def _lib():
     """The library with its moe_ functions declared."""
     if not _fns:
         lib = _declare(load())
-        _fns.update((name, getattr(lib, name)) for name in MOE_EXPORTED)
+        # all at once: another thread may be looking
+        _fns.update({name: getattr(lib, name) for name in MOE_EXPORTED})
     return load()
 
 

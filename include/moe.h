@@ -111,12 +111,11 @@ enum {
  *   out_scales    SWIGLU: [groups][cap][n / 256] float; else NULL.
  * Rows past a group's count are neither read nor written. k: a positive
  * multiple of 128; n: a positive multiple of 8 (ROWS) or 256 (SWIGLU); n, k
- * and groups at most 2^20, groups, cap >= 0. A row's result depends on its own inputs
- * alone. a, b and out 16-byte aligned, the rest 4-byte.
- * Errors: EP_ERR_NULL, EP_ERR_ALIGN, EP_ERR_ARG, EP_ERR_SIZE (n or k too
- * large, groups * cap above 2^31 - 1, or more than 2^31 - 1 row tiles of 256),
- * EP_ERR_HIP. groups == 0 or cap == 0 returns EP_OK whatever the pointers
- * are. */
+ * and groups at most 2^20, groups, cap >= 0. A row's result depends on its own
+ * inputs alone. a, b and out 16-byte aligned, the rest 4-byte.
+ * Errors: EP_ERR_NULL, EP_ERR_ALIGN, EP_ERR_ARG, EP_ERR_SIZE (n, k or groups
+ * too large, or groups * cap above 2^31 - 1), EP_ERR_HIP. groups == 0 or cap
+ * == 0 returns EP_OK whatever the pointers are. */
 typedef struct moe_grouped_gemm_args {
     const void *a;
     const float *a_scales;

@@ -196,3 +196,16 @@ def test_grouped_gemm_without_rows_is_no_work(lib):
     for change in (dict(groups=0), dict(cap=0)):
         args = gemm_args(a=None, out=None, **change)
         assert lib.moe_grouped_gemm(ctypes.byref(args), None) == cra.EP_OK
+
+
+def test_backward_of_another_devices_tensors_is_refused():
+    import torch
+    from types import SimpleNamespace as Fields
+    op = Fields(_ex={"plan": 0}, workspace=Fields(device=torch.device("cuda:0")))
+    state = cra.EpDispatchCombineOp._fused_state
+    assert state(op, "call", Fields(device=torch.device("cuda:0")), "grad_out") is op._ex
+    with pytest.raises(ValueError, match="grad_out is on cuda:1, the op on cuda:0"):
+        state(op, "call", Fields(device=torch.device("cuda:1")), "grad_out")
+    op._ex = None
+    with pytest.raises(cra.EpError, match="before any dispatch_standard_moe"):
+        state(op, "call", Fields(device=torch.device("cuda:0")), "grad_out")
