@@ -846,11 +846,9 @@ class EpDispatchCombineOp:
         # may hold them
         bufs = ex.setdefault("mlp", {})
         if inter not in bufs:
-            dev = self.workspace.device
-            bufs[inter] = (torch.empty((G, cap, inter), dtype=torch.uint8, device=dev),
-                           torch.empty((G, cap, inter // 128), dtype=torch.float32, device=dev),
-                           torch.empty((W, Er, cap, H), dtype=_TORCH[cfg.combine_dtype],
-                                       device=dev))
+            bufs[inter] = (self._new((G, cap, inter), torch.uint8, stream),
+                           self._new((G, cap, inter // 128), torch.float32, stream),
+                           self._new((W, Er, cap, H), _TORCH[cfg.combine_dtype], stream))
         hidden, hidden_scales, y = bufs[inter]
         counts = packed_recv_count.view(G)
         moe_grouped_gemm_swiglu(rows.view(G, cap, H), scales.view(torch.float32).view(
@@ -893,15 +891,19 @@ class EpDispatchCombineOp:
         moe_dispatch_backward(ex["plan"], cfg, self.expert_capacity, grad_packed_x, grad_x, stream)
         return grad_x
 
-    def _zeros(self, shape, dtype, stream):
-        """New zeros, filled (and owned by torch's allocator) on the stream
-        the call runs on."""
+    def _new(self, shape, dtype, stream, make=torch.empty):
+        """A new tensor, owned by torch's allocator (and filled) on the stream
+        the call runs on: its memory may have had a use before that is pending
+        on the stream it was of."""
         if stream is None:
-            return torch.zeros(shape, dtype=dtype, device=self.workspace.device)
+            return make(shape, dtype=dtype, device=self.workspace.device)
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=self.workspace.device)
         with torch.cuda.stream(stream):
-            return torch.zeros(shape, dtype=dtype, device=self.workspace.device)
+            return make(shape, dtype=dtype, device=self.workspace.device)
+
+    def _zeros(self, shape, dtype, stream):
+        return self._new(shape, dtype, stream, torch.zeros)
 
     def _fused_state(self, call, given, name):
         """The expert plan's state for a call on tensors that lie with `given`:

@@ -133,3 +133,32 @@ def test_expert_mlp_refuses():
     plain = cra.EpDispatchCombineOp(cra.make_config(2, 256, 20, 4, 3), expert_capacity=16)
     with pytest.raises(ValueError, match="fp8"):
         plain.expert_mlp(px, count, t["gu"], t["gus"], t["dn"], t["dns"])
+
+
+def test_expert_mlp_on_a_stream_takes_no_memory_still_in_use():
+    """New buffers of a call on another stream do not lie over memory whose
+    last use is pending on torch's current one."""
+    d = setup(seed=4)
+    want = layer(d).clone()
+    t, op = d["dev"], d["op"]
+    px, count, _, _ = op.dispatch_standard_moe(d["codes"], None, d["scales"], t["ids"], d["ntok"])
+    hidden, hidden_scales, y = op._expert_state().pop("mlp")[128]
+    wants = y.clone()
+    sizes = [(v.shape, v.dtype) for v in (hidden, hidden_scales, y)]
+    del hidden, hidden_scales, y
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    used = [torch.empty(shape, dtype=dt, device="cuda") for shape, dt in sizes]
+    torch.cuda._sleep(20_000_000)
+    for v in used:
+        v.fill_(1)
+    del used, v
+    y = op.expert_mlp(px, count, t["gu"], t["gus"], t["dn"], t["dns"], stream=s)
+    torch.cuda.synchronize()
+    n = count.flatten().tolist()
+    for g, c in enumerate(n):
+        assert torch.equal(y.view(len(n), -1, d["H"])[g, :c], wants.view(len(n), -1, d["H"])[g, :c])
+    out = op.combine_standard_moe(y, t["w"], t["ids"])
+    for r in range(d["W"]):
+        assert torch.equal(out[r, :d["ntok"][r]], want[r, :d["ntok"][r]])
