@@ -35,7 +35,9 @@ using namespace moe::dev;
 using ep::kWave;
 using ep::TokenMap;
 
-// kDot: the weights' gradient is asked for (and the pairs' rows are read).
+// kDot: the weights' gradient is asked for (and the pairs' rows are read). A
+// block row of the grid takes group_slots of the tokens' slots: the pairs of a
+// token are independent of each other.
 template <int DT, bool kDot, bool kStream>
 __global__ __launch_bounds__(kBackMaxWaves * kWave) void moe_combine_backward_kernel(
     CombineBackwardArgs a, TokenMap tk)
@@ -84,7 +86,9 @@ __global__ __launch_bounds__(kBackMaxWaves * kWave) void moe_combine_backward_ke
     const uint32_t bytes = (uint32_t)a.row_vecs * 16u;
     const __amdgpu_buffer_rsrc_t rgo = row_rsrc(a.go + (mine ? tok : 0) * (int64_t)bytes,
                                                 mine ? bytes : 0u);
-    const uint64_t kept = __ballot(row >= 0);
+    const int slot0 = (int)blockIdx.y * a.group_slots;
+    const uint64_t group = (~0ull >> (kWave - a.group_slots)) << slot0;
+    const uint64_t kept = __ballot(row >= 0) & group;
     const int vbeg = part * a.wave_vecs;
     const int vend = min(a.row_vecs, vbeg + a.wave_vecs);
     for (int v0 = vbeg; v0 < vend && kept != 0; v0 += kWave * C) {
@@ -150,7 +154,7 @@ __global__ __launch_bounds__(kBackMaxWaves * kWave) void moe_combine_backward_ke
     }
     if constexpr (kDot) {
         __syncthreads();
-        if (part == 0 && has) {
+        if (part == 0 && has && (group >> first & 1)) {
             float g = 0.0f;
             for (int i = 0; i < a.row_waves; ++i)
                 g = g + s_dot[wave + i][first];
@@ -217,11 +221,13 @@ hipError_t launch_combine_backward(const CombineBackwardArgs& a, const TokenMap&
     if (tk.total == 0)
         return hipSuccess;
     if (a.row_waves < 1 || a.row_waves > kBackMaxWaves || a.k > ep::kMaxTopk ||
+        a.group_slots < 1 || a.group_slots > kWave ||
         (int64_t)a.row_waves * a.wave_vecs < a.row_vecs)
         return hipErrorInvalidValue;
     const int waves = a.row_waves > 4 ? a.row_waves : 4;
     const int block_tokens = waves / a.row_waves;
-    const dim3 grid((unsigned)((tk.total + block_tokens - 1) / block_tokens));
+    const dim3 grid((unsigned)((tk.total + block_tokens - 1) / block_tokens),
+                    (unsigned)((a.k + a.group_slots - 1) / a.group_slots));
     const dim3 block(waves * kWave);
     if (dtype == 0) {
         if (a.gw)

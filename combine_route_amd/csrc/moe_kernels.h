@@ -56,6 +56,7 @@ struct CombineBackwardArgs {
     int32_t row_vecs;            // 16-byte vectors a row
     int32_t row_waves;           // waves a token: a power of two up to kBackMaxWaves
     int32_t wave_vecs;           // vectors of a wave's share of the row
+    int32_t group_slots;         // slots a wave handles, 1 .. 64
     int32_t M, k, E;
 };
 

@@ -281,3 +281,20 @@ def test_graph_and_stream():
     written = torch.zeros((c.E * c.cap, 1), dtype=torch.bool, device="cuda")
     written[c.pairs()[3].cuda()] = True
     assert torch.equal(gy.view(-1, c.H), torch.where(written, want[0].view(-1, c.H), 0))
+
+
+@pytest.mark.parametrize("ids", ["distinct", "any"])
+def test_few_tokens_give_the_bits_of_many(ids):
+    """A call of few tokens takes their slots in groups, one of many takes them
+    together: the first tokens' results (their rows are the experts' first)
+    are the same bits."""
+    many = Case(1, 2100, 1000, 64, 80, 2100, "bf16", ids=ids, seed=7)
+    gy, gw = many.combine_backward()
+    for n in (1, 3, 40):
+        few = Case(1, 2100, 1000, 64, 80, 2100, "bf16", ntok=[n], ids=ids, seed=7)
+        assert torch.equal(few.ids, many.ids) and torch.equal(few.y, many.y)
+        fy, fw = few.combine_backward()
+        assert torch.equal(fw[:, :n], gw[:, :n]) and bool((fw[:, n:] == 7).all())
+        p = few.pairs()[3]
+        assert torch.equal(few.rows[:, :n], many.rows[:, :n])
+        assert torch.equal(fy.view(-1, few.H)[p], gy.view(-1, few.H)[p])
