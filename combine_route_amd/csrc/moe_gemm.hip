@@ -8,8 +8,8 @@
 // Row counts are on the GPU, so the launch is a fixed grid of one block a
 // compute unit; each block works out every expert's tile range from the
 // counts and walks its share of the tiles. An expert's last tile computes as
-// few of 64, 128 or 224 rows as hold its rows, so that experts with few rows
-// cost their weights' bytes and little else.
+// few of 32 (swiglu form), 64, 128 or 224 rows as hold its rows, so that experts
+// with few rows cost their weights' bytes and little else.
 //
 // The FP8 matrix instruction adds 8 products at a time after aligning them to
 // the largest of the 8 and cutting what lies below 2^-13 of it (measured on
@@ -21,12 +21,12 @@
 // (exact) in registers and multiplied by v_mfma_f32_16x16x32_f16, whose sums
 // of such products are FP32's (scales off by 2e-7); the matrix rate is half.
 //
-// Inside a tile: 8 waves, 2 along the rows x 4 along the weight rows. For
-// each 128 elements of k (a step) the block holds both operands' slices (128
-// bytes a row) in LDS, loaded there directly from memory two steps and more
-// before. The matrix instruction has the weights as its rows and the token
-// rows as its columns: v_mfma_f32_16x16x128_f8f6f4 takes a whole scale block
-// of k, a lane then holds one token row's partial sums, so the scales'
+// Inside a tile: 8 waves, 2 along the rows x 4 along the weight rows (1 x 8 of
+// 32 rows). For each 128 elements of k (a step) the block holds both operands'
+// slices (128 bytes a row) in LDS, loaded there directly from memory two steps
+// and more before. The matrix instruction has the weights as its rows and the
+// token rows as its columns: v_mfma_f32_16x16x128_f8f6f4 takes a whole scale
+// block of k, a lane then holds one token row's partial sums, so the scales'
 // product is one value a lane and the partial joins the FP32 sum with a fused
 // multiply-add an element, beside the next matrix instruction. 224 rows: the
 // largest tile whose rows' slices fit LDS three times beside two of the
@@ -76,26 +76,35 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int kThreads = 512;
 constexpr int kTileN = 256;                     // weight rows a tile
 constexpr int kSlice = 128;                     // bytes of k a step
-constexpr int kWaveRows = 64;                   // weight rows a wave
-constexpr int kSubs = kWaveRows / 16;           // 16-row operands of them
 constexpr int kBLoads = kTileN / 64;            // 16-byte loads a lane and weight slice
 
-// Token rows of a tile whose waves hold TS operands of 16 rows each, and its
-// place in LDS: kAStages slices of the rows, b_stages of the weights, and two
-// blocks of scales (4 steps of every row, then of the tile's two weight
-// blocks).
+// A tile of class TS has 32 TS token rows. Its waves lie 2 along the rows and 4
+// along the weight rows; those of 32 rows 1 and 8, so that each weight row is
+// read from LDS (and widened) once. A wave holds row_subs operands of 16 token
+// rows and col_subs of 16 weight rows.
 constexpr int kMaxTS = 7;
-constexpr int tile_rows(int ts) { return 2 * 16 * ts; }
+constexpr int row_waves(int ts) { return ts == 1 ? 1 : 2; }
+constexpr int col_waves(int ts) { return ts == 1 ? 8 : 4; }
+constexpr int row_subs(int ts) { return 2 * ts / row_waves(ts); }
+constexpr int col_subs(int ts) { return kTileN / 16 / col_waves(ts); }
+constexpr int tile_rows(int ts) { return 32 * ts; }
+// Its place in LDS: kAStages slices of the rows, b_stages of the weights, and
+// two blocks of scales (4 steps of every row, then of the tile's two weight
+// blocks), of which the second holds the col_waves' block maxima at the end.
 constexpr int kTileRows = tile_rows(kMaxTS);
 constexpr int kAStages = 3;
 constexpr int b_stages(int ts) { return ts == 7 ? 2 : ts == 4 ? 3 : 4; }
 constexpr int a_bytes(int ts) { return tile_rows(ts) * kSlice; }
 constexpr int kBBytes = kTileN * kSlice;
-constexpr int scale_bytes(int ts) { return (tile_rows(ts) + 2) * 16; }
+constexpr int scale_bytes(int ts)
+{
+    return ts == 1 ? col_waves(ts) * 4 * tile_rows(ts) : (tile_rows(ts) + 2) * 16;
+}
 constexpr int scale_at(int ts) { return kAStages * a_bytes(ts) + b_stages(ts) * kBBytes; }
 constexpr int lds_bytes(int ts) { return scale_at(ts) + 2 * scale_bytes(ts); }
 constexpr int kLdsBytes = lds_bytes(7);
-static_assert(lds_bytes(4) <= kLdsBytes && lds_bytes(2) <= kLdsBytes, "LDS of a block");
+static_assert(lds_bytes(4) <= kLdsBytes && lds_bytes(2) <= kLdsBytes && lds_bytes(1) <= kLdsBytes,
+              "LDS of a block");
 
 // The end of a phase: this wave's LDS reads have returned and at most N of its
 // loads are in flight; then the same holds for every wave.
@@ -377,26 +386,34 @@ struct Loads {
 // spread among them: issued together they hold up the waves, which issue in
 // order, until the load unit has taken them.
 template <int TS, bool kSwiglu>
-__device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, f32x4 (&acc)[TS][kSubs])
+__device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
+                                         f32x4 (&acc)[row_subs(TS)][col_subs(TS)])
 {
     using L = Loads<TS, kSwiglu>;
+    constexpr int kRowSubs = row_subs(TS), kSubs = col_subs(TS);
     constexpr int SB = L::SB;
     const uint8_t* lds = ld.lds;
     const int lane = threadIdx.x & (kWave - 1);
-    const int wm = ld.wave >> 2, wn = ld.wave & 3;
+    const int wm = ld.wave / col_waves(TS), wn = ld.wave % col_waves(TS);
     const int q = lane >> 4, i16 = lane & 15;
     // a lane's row of each operand, its chunks q and q + 4 (exclusive-or 4)
-    const int wrow = wn * (kSwiglu ? 32 : kWaveRows) + 8 * (i16 >> 2) + (i16 & 3);
+    // (gate rows in the swiglu form; its up rows are 128 further)
+    const int wrow = (!kSwiglu     ? wn * 16 * kSubs
+                      : kSubs == 4 ? wn * 32
+                                   : (wn >> 1) * 32 + (wn & 1) * 4) +
+                     8 * (i16 >> 2) + (i16 & 3);
     const int wkey = (wrow & 3) | (((wrow >> 3) & 1) << 2);
     const uint32_t wlo = L::kB + (uint32_t)wrow * kSlice + (uint32_t)((q ^ wkey) * 16);
-    const int trow = wm * 16 * TS + i16;
+    const int trow = wm * 16 * kRowSubs + i16;
     const uint32_t tlo = (uint32_t)trow * kSlice + (uint32_t)((q ^ (trow & 7)) * 16);
     auto sub_offset = [](int s) {
-        return (uint32_t)((s & 1) * 4 + (s >> 1) * (kSwiglu ? 128 : 32)) * kSlice;
+        return (uint32_t)(kSwiglu && kSubs == 2 ? s * 128
+                                                : (s & 1) * 4 + (s >> 1) * (kSwiglu ? 128 : 32)) *
+               kSlice;
     };
 
 #pragma unroll
-    for (int j = 0; j < TS; ++j)
+    for (int j = 0; j < kRowSubs; ++j)
 #pragma unroll
         for (int s = 0; s < kSubs; ++s)
             acc[j][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -433,7 +450,7 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, f32x4 (&a
         const float* scale =
             reinterpret_cast<const float*>(lds + L::kScale + ((kb >> 2) & 1) * scale_bytes(TS)) +
             (kb - ld.scale_start(kb));
-        const float wb0 = scale[(L::kRows + (kSwiglu ? 0 : wn >> 1)) * 4];
+        const float wb0 = scale[(L::kRows + (kSwiglu ? 0 : wn / (col_waves(TS) / 2))) * 4];
         const float wb1 = kSwiglu ? scale[(L::kRows + 1) * 4] : wb0;
         float sx = scale[trow * 4];
         i32x4 lo = tokens(0, 0), hi = tokens(0, 1);
@@ -452,17 +469,17 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, f32x4 (&a
         auto asks = [&](int j) {  // the loads of operand j's turn
 #pragma unroll
             for (int i = 0; i < L::kAll; ++i)
-                if (i * TS / L::kAll == j)
+                if (i * kRowSubs / L::kAll == j)
                     ask(i);
         };
         f32x4 old[kSubs];  // the products of operand j - 1
         float oldc0 = 0.0f, oldc1 = 0.0f;
         if constexpr (!kSwiglu) {
 #pragma unroll
-            for (int j = 0; j < TS; ++j) {
+            for (int j = 0; j < kRowSubs; ++j) {
                 const i32x8 x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                 const float c = sx * wb0;
-                if (j + 1 < TS) {
+                if (j + 1 < kRowSubs) {
                     lo = tokens(j + 1, 0);
                     hi = tokens(j + 1, 1);
                     sx = scale[(trow + (j + 1) * 16) * 4];
@@ -488,7 +505,7 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, f32x4 (&a
             oldc1 = oldc0;
         } else {
 #pragma unroll
-            for (int j = 0; j < TS; ++j) {
+            for (int j = 0; j < kRowSubs; ++j) {
                 const float c0 = sx * wb0, c1 = sx * wb1;
                 f32x4 p[kSubs];
 #pragma unroll
@@ -498,18 +515,23 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, f32x4 (&a
                         p[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                             v[s].v[h], __builtin_bit_cast(f16x8, y[h & 1]),
                             h == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p[s], 0, 0, 0);
-                        // one value pair of the next operand
-                        if (h < 3)
-                            y[(h + 1) & 1][s] = widened2(h == 0 ? lo : hi, h + 1, s);
-                        else if (j + 1 < TS)
-                            y[0][s] = widened2(lo, 0, s);
+                        // its share of the next operand's value pairs
+#pragma unroll
+                        for (int i = s * 4 / kSubs; i < (s + 1) * 4 / kSubs; ++i) {
+                            if (h < 3)
+                                y[(h + 1) & 1][i] = widened2(h == 0 ? lo : hi, h + 1, i);
+                            else if (j + 1 < kRowSubs)
+                                y[0][i] = widened2(lo, 0, i);
+                        }
                         // and one sum of the products before
-                        if (j > 0)
-                            acc[j - 1][h][s] =
-                                __builtin_fmaf(old[h][s], h < 2 ? oldc0 : oldc1, acc[j - 1][h][s]);
+                        if (j > 0) {
+                            const int c = (h * kSubs + s) / 4, r = (h * kSubs + s) % 4;
+                            acc[j - 1][c][r] = __builtin_fmaf(
+                                old[c][r], c < kSubs / 2 ? oldc0 : oldc1, acc[j - 1][c][r]);
+                        }
                         __builtin_amdgcn_sched_barrier(0);
                     }
-                    if (j + 1 < TS) {  // the halves are read again as soon as they are widened
+                    if (j + 1 < kRowSubs) {  // the halves are read again as soon as they are widened
                         if (h == 0)
                             lo = tokens(j + 1, 0);
                         if (h == 2)
@@ -531,8 +553,8 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, f32x4 (&a
         for (int s = 0; s < kSubs; ++s)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                acc[TS - 1][s][r] =
-                    __builtin_fmaf(old[s][r], s < 2 ? oldc0 : oldc1, acc[TS - 1][s][r]);
+                acc[kRowSubs - 1][s][r] = __builtin_fmaf(
+                    old[s][r], s < kSubs / 2 ? oldc0 : oldc1, acc[kRowSubs - 1][s][r]);
         sta = sta == 2 ? 0 : sta + 1;
         stb = stb + 1 == SB ? 0 : stb + 1;
     }
@@ -542,28 +564,29 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, f32x4 (&a
 // The tile's sums to memory.
 template <int TS, int DT, bool kSwiglu>
 __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (*s_amax)[tile_rows(TS)],
-                                       f32x4 (&acc)[TS][kSubs])
+                                       f32x4 (&acc)[row_subs(TS)][col_subs(TS)])
 {
+    constexpr int kRowSubs = row_subs(TS), kSubs = col_subs(TS);
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / col_waves(TS), wn = wave % col_waves(TS);
     const int q = lane >> 4;
-    const int trow0 = wm * 16 * TS + (lane & 15);
+    const int trow0 = wm * 16 * kRowSubs + (lane & 15);
     // ---- epilogue
     if constexpr (!kSwiglu) {
-        // a lane holds two runs of 8 columns of each of its rows; the 4 lanes of
+        // a lane holds runs of 8 columns of each of its rows; the 4 lanes of
         // a row write 64 bytes together. Rows few and far between are written
         // through the L2 (sc1), which the weights stream through (256 experts x
         // 32 rows, k 2048, n 7168: 716 -> 680 us).
         constexpr int kStore = TS < kMaxTS ? 16 : 0;
-        const int col = t.col * kTileN + wn * kWaveRows + q * 8;
+        const int col = t.col * kTileN + wn * 16 * kSubs + q * 8;
         const __amdgpu_buffer_rsrc_t ro =
             uniform_rsrc(a.out + t.row0 * a.n * 2, (uint32_t)t.rows * (uint32_t)a.n * 2u);
 #pragma unroll
-        for (int j = 0; j < TS; ++j) {
+        for (int j = 0; j < kRowSubs; ++j) {
             const uint32_t at = ((uint32_t)(trow0 + j * 16) * (uint32_t)a.n + (uint32_t)col) * 2u;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < kSubs / 2; ++h) {
                 float f[8];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -575,20 +598,21 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
             }
         }
     } else {
-        // gate in operands 0 and 1, up in 2 and 3: a lane holds 8 consecutive
-        // values of each of its rows, the wave 32, the four waves the block
+        // gate in the first half of the operands, up in the second: a lane holds
+        // 8 (4 of 2 operands) consecutive values of each of its rows
+        constexpr int kGate = kSubs / 2;
 #pragma unroll
-        for (int j = 0; j < TS; ++j) {
+        for (int j = 0; j < kRowSubs; ++j) {
             float amax = 0.0f;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < kGate; ++s) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float g = acc[j][s][r];
                     // both sides of the quotient over 16, so that the reciprocal
                     // stays in the normal range wherever the exponential is finite
                     const float d = __builtin_fmaf(__expf(-g), 0.0625f, 0.0625f);
-                    const float z = g * 0.0625f * __builtin_amdgcn_rcpf(d) * acc[j][2 + s][r];
+                    const float z = g * 0.0625f * __builtin_amdgcn_rcpf(d) * acc[j][kGate + s][r];
                     acc[j][s][r] = z;
                     amax = __builtin_fmaxf(amax, __builtin_fabsf(z));
                 }
@@ -600,24 +624,31 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
         }
         phase_end();
         const int inter = a.n / 2;
-        const int col = t.col * 128 + wn * 32 + q * 8;
+        const int col =
+            t.col * 128 + q * 8 + (kGate == 2 ? wn * 32 : (wn >> 1) * 32 + (wn & 1) * 4);
         const __amdgpu_buffer_rsrc_t ro =
             uniform_rsrc(a.out + t.row0 * inter, (uint32_t)t.rows * (uint32_t)inter);
         const uint32_t orow = (uint32_t)(inter / 128) * 4u;
         const __amdgpu_buffer_rsrc_t rsc =
             uniform_rsrc(a.osc + t.row0 * orow, (uint32_t)t.rows * orow);
 #pragma unroll
-        for (int j = 0; j < TS; ++j) {
+        for (int j = 0; j < kRowSubs; ++j) {
             const int row = trow0 + j * 16;
-            const float amax = __builtin_fmaxf(__builtin_fmaxf(s_amax[0][row], s_amax[1][row]),
-                                               __builtin_fmaxf(s_amax[2][row], s_amax[3][row]));
+            float amax = s_amax[0][row];
+#pragma unroll
+            for (int w = 1; w < col_waves(TS); ++w)
+                amax = __builtin_fmaxf(amax, s_amax[w][row]);
             float s, f;
             block_scale(amax, &s, &f);
-            const u32x2 c = {e4m3x4(acc[j][0][0] * f, acc[j][0][1] * f, acc[j][0][2] * f,
-                                    acc[j][0][3] * f),
-                             e4m3x4(acc[j][1][0] * f, acc[j][1][1] * f, acc[j][1][2] * f,
-                                    acc[j][1][3] * f)};
-            __builtin_amdgcn_raw_buffer_store_b64(c, ro, row * inter + col, 0, 0);
+            uint32_t c[kGate];
+#pragma unroll
+            for (int s = 0; s < kGate; ++s)
+                c[s] = e4m3x4(acc[j][s][0] * f, acc[j][s][1] * f, acc[j][s][2] * f,
+                              acc[j][s][3] * f);
+            if constexpr (kGate == 2)
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{c[0], c[1]}, ro, row * inter + col, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b32(c[0], ro, row * inter + col, 0, 0);
             if (wn == 0 && q == 0)
                 __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, s), rsc,
                                                       row * orow + t.col * 4, 0, 0);
@@ -625,8 +656,16 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
     }
 }
 
-// Operands of 16 rows a wave that a tile of this many rows needs.
-__device__ __forceinline__ int tile_class(int rows) { return rows > 128 ? 7 : rows > 64 ? 4 : 2; }
+// The class of a tile with this many rows. The class of 32 rows is the swiglu
+// form's alone: what it saves is the widening (222 experts x 1 to 9 rows, k
+// 6272, n 512: 149 -> 134 us; 27 x 4 rows, k 4608, n 256: 50 -> 38), and in the
+// other form a change of class between tiles, whose loads then start late,
+// costs more than it gains (256 experts x 16 to 48 rows: 684 -> 698 us).
+template <bool kSwiglu>
+__device__ __forceinline__ int tile_class(int rows)
+{
+    return rows > 128 ? 7 : rows > 64 ? 4 : rows > 32 || !kSwiglu ? 2 : 1;
+}
 
 template <int DT, bool kSwiglu>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void
@@ -741,14 +780,14 @@ moe_gemm_kernel(GemmArgs a)
         slot ^= 1;
         if (next >= 0)
             look_up(next, s_tile[slot]);  // read after the steps' barriers
-        f32x4 acc[TS][kSubs];
+        f32x4 acc[row_subs(TS)][col_subs(TS)];
         multiply<TS, kSwiglu>(ld, acc);
         const Tile done = t;
         t.rows = 0;
         loading = false;
         if (next >= 0) {
             t = read_tile(s_tile[slot]);
-            if (tile_class(t.rows) == TS) {
+            if (tile_class<kSwiglu>(t.rows) == TS) {
                 // the next tile's loads run under this one's stores
                 const Loads<TS, kSwiglu> then(a, t, lds, lds0);
                 then.prologue();
@@ -757,15 +796,23 @@ moe_gemm_kernel(GemmArgs a)
         }
         // the block maxima go where the second block of scales was: the next
         // tile asks for that one after its first phases
-        static_assert(scale_bytes(TS) >= (int)sizeof(float) * 4 * tile_rows(TS), "block maxima");
+        static_assert(scale_bytes(TS) >= (tile_rows(TS) + 2) * 16 &&
+                          scale_bytes(TS) >= (int)sizeof(float) * col_waves(TS) * tile_rows(TS),
+                      "scales, block maxima");
         finish<TS, DT, kSwiglu>(
             a, done,
             reinterpret_cast<float(*)[tile_rows(TS)]>(lds + scale_at(TS) + scale_bytes(TS)), acc);
     };
     while (t.rows > 0) {
-        switch (tile_class(t.rows)) {
+        switch (tile_class<kSwiglu>(t.rows)) {
         case 7: run(std::integral_constant<int, 7>()); break;
         case 4: run(std::integral_constant<int, 4>()); break;
+        case 1:
+            if constexpr (kSwiglu) {
+                run(std::integral_constant<int, 1>());
+                break;
+            }
+            [[fallthrough]];  // the other form has no such tile
         default: run(std::integral_constant<int, 2>()); break;
         }
     }

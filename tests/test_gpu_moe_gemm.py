@@ -360,3 +360,18 @@ def test_streams_and_graph():
         assert bool((out[g, g + 1:] == 7).all())
         assert torch.equal(out[g, :g + 1][:int(min(g + 1, [100, 0, 33, 64][g]))],
                            want[g, :g + 1][:int(min(g + 1, [100, 0, 33, 64][g]))])
+
+
+@pytest.mark.parametrize("k", [128, 256, 384, 512, 640, 1152])
+def test_few_rows_swiglu(k):
+    """The smallest tile: against the formula, and the bits of a larger one."""
+    counts = [1, 15, 16, 17, 31, 32, 33]
+    inp = inputs(len(counts), 70, 512, k, seed=k + 1)
+    codes, scales = (v.cpu() for v in run_swiglu(inp, device_counts(counts)))
+    wc, ws = (v.cpu() for v in run_swiglu(inp, None))
+    y, size = product(*inp)
+    z, err = swiglu(y, size, k)
+    for g, c in enumerate(counts):
+        assert torch.equal(codes[g, :c], wc[g, :c]) and torch.equal(scales[g, :c], ws[g, :c])
+        ref.quantized_close(codes[g, :c], scales[g, :c], z[g, :c], 0.0, err[g, :c])
+        assert bool((codes[g, c:] == 77).all()) and bool((scales[g, c:] == 7).all())
