@@ -94,6 +94,8 @@ constexpr int tile_rows(int ts) { return 32 * ts; }
 constexpr int kTileRows = tile_rows(kMaxTS);
 constexpr int kAStages = 3;
 constexpr int b_stages(int ts) { return ts == 7 ? 2 : ts == 4 ? 3 : 4; }
+// Whether a step has one barrier, see multiply().
+constexpr bool one_barrier(int ts, bool swiglu) { return swiglu && ts < kMaxTS; }
 constexpr int a_bytes(int ts) { return tile_rows(ts) * kSlice; }
 constexpr int kBBytes = kTileN * kSlice;
 constexpr int scale_bytes(int ts)
@@ -246,6 +248,8 @@ struct Tile {
 template <int TS, bool kSwiglu>
 struct Loads {
     static constexpr int SB = b_stages(TS);
+    static constexpr bool kOneBarrier = one_barrier(TS, kSwiglu);
+    static constexpr int kLead = kOneBarrier ? SB - 1 : SB;  // steps the weights are ahead
     static constexpr int kRows = tile_rows(TS);
     static constexpr int kALoads = (kRows + 63) / 64;       // loads a wave and slice of rows
     static constexpr int kAll = kALoads + kBLoads;          // and of both
@@ -364,7 +368,7 @@ struct Loads {
                 weight_load(i, kb, kb);
         };
 #pragma unroll
-        for (int kb = 0; kb < SB - 2; ++kb)
+        for (int kb = 0; kb < kLead - 2; ++kb)
             weights(kb);
         scales(0);
 #pragma unroll
@@ -372,7 +376,7 @@ struct Loads {
 #pragma unroll
             for (int i = 0; i < kALoads; ++i)
                 row_load(i, kb, kb);
-            weights(SB - 2 + kb);
+            weights(kLead - 2 + kb);
         }
     }
 };
@@ -381,10 +385,14 @@ struct Loads {
 // barriers. The first waits for the step's slices and ends the reads of the
 // step before, so the place of the rows' slice kb - 1 is free for slice kb +
 // 2. Then every wave takes its weights' operands to registers; the second
-// barrier frees their place for slice kb + SB. The products follow, each
-// matrix instruction with as much other work as runs beside it, and the loads
-// spread among them: issued together they hold up the waves, which issue in
-// order, until the load unit has taken them.
+// barrier frees their place for slice kb + SB. In the swiglu form's smaller
+// tiles there is none: the weights' slice kb + SB - 1 goes where slice kb - 1
+// was, and a wave may read while another multiplies (27 experts x 4 rows, k
+// 4608, n 256: 38 -> 34 us; 32 x 32 rows, k 7168, n 4096: 180 -> 176; in the
+// other form, 256 x 32 rows, k 2048, n 7168, 684 -> 690).
+// The products follow, each matrix instruction with as much other work as runs
+// beside it, and the loads spread among them: issued together they hold up the
+// waves, which issue in order, until the load unit has taken them.
 template <int TS, bool kSwiglu>
 __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
                                          f32x4 (&acc)[row_subs(TS)][col_subs(TS)])
@@ -420,9 +428,9 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
 
     const int nk = ld.nk;
     // Loads a wave has in flight when a step starts, of those asked for after
-    // the step's rows (with two stages its weights come after them). Scales
+    // the step's rows (two steps ahead its weights come after them). Scales
     // come on top now and then, which only makes the wait stricter.
-    constexpr int kLater = SB > 2 ? L::kAll + kBLoads : L::kAll;
+    constexpr int kLater = L::kLead > 2 ? L::kAll + kBLoads : L::kAll;
 
     int sta = 0, stb = 0;  // stages of step kb
     for (int kb = 0; kb < nk; ++kb) {
@@ -436,12 +444,13 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
         phase_end<kLater>();
         ld.scales(kb + 2);
         const int free_a = sta == 0 ? 2 : sta - 1;
+        const int free_b = !L::kOneBarrier ? stb : stb == 0 ? SB - 1 : stb - 1;
         // load `i` of the step's, rows first
         auto ask = [&](int i) {
             if (i < L::kALoads)
                 ld.row_load(i, kb + 2, free_a);
             else
-                ld.weight_load(i - L::kALoads, kb + SB, stb);
+                ld.weight_load(i - L::kALoads, kb + L::kLead, free_b);
         };
         i32x8 w[kSubs];
 #pragma unroll
@@ -454,7 +463,8 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
         const float wb1 = kSwiglu ? scale[(L::kRows + 1) * 4] : wb0;
         float sx = scale[trow * 4];
         i32x4 lo = tokens(0, 0), hi = tokens(0, 1);
-        phase_end();
+        if constexpr (!L::kOneBarrier)
+            phase_end();
         Widened v[kSwiglu ? kSubs : 1];
         u32x4 y[2];  // operands of 8 values, in turn
         if constexpr (kSwiglu) {
