@@ -41,13 +41,15 @@
 // Measured on MI355X (a large FP8 library product: 2.6 PFLOP/s, bf16 1.35;
 // weights streamed to LDS alone: 7.0 TB/s): 32 experts x 1024 rows, n 7168, k
 // 2048 545 us (1.77 PFLOP/s), n 4096, k 7168 960 us (2.0); gate and up, n
-// 4096, k 7168, 32768 rows in all 1.7 to 1.8 ms (1.1 PFLOP/s in fp16
+// 4096, k 7168, 32768 rows in all 1.6 to 1.8 ms (1.1 PFLOP/s in fp16
 // products; without its loads 1.4 ms). Large tiles are bound by the matrix
 // units' power and the sums beside them: without their loads they take 780 us
 // instead of 960. 256 experts x 32 rows, n 7168, k 2048 680 us (5.7 TB/s; 545
 // without its stores: 117 MB of scattered rows in a stream of reads), gate and
-// up of 32 experts x 32 rows 182 us (5.2 TB/s): bound by memory. Tried and no
-// faster: the wave halves taking turns at reading and multiplying (1108
+// up of 32 experts x 32 rows 177 us (5.3 TB/s; its loads alone 143, its products
+// and conversions alone 145): bound by memory and the phases of a step that do
+// not run beside each other. Tried and no faster: widening by shifts and masks
+// instead of conversions (221 against 180 us), the wave halves taking turns at reading and multiplying (1108
 // against 1010 us), raised wave priority, a step's loads all in its first
 // products (980 against 950 us), products of 32 x 32 x 16 in the swiglu form
 // (2.0 ms: a product's 32 sums run in one piece), operands a step ahead in
