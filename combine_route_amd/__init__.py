@@ -910,7 +910,8 @@ class EpDispatchCombineOp:
         the plan's map is on the op's own device."""
         if self._ex is None:
             raise EpError(call, EP_ERR_STATE, f"{call} before any dispatch_standard_moe")
-        if given.device != self.workspace.device:
+        # (what is no tensor is refused by the call itself)
+        if getattr(given, "device", self.workspace.device) != self.workspace.device:
             raise ValueError(f"{name} is on {given.device}, the op on {self.workspace.device}")
         return self._ex
 

@@ -206,6 +206,7 @@ def test_backward_of_another_devices_tensors_is_refused():
     assert state(op, "call", Fields(device=torch.device("cuda:0")), "grad_out") is op._ex
     with pytest.raises(ValueError, match="grad_out is on cuda:1, the op on cuda:0"):
         state(op, "call", Fields(device=torch.device("cuda:1")), "grad_out")
+    assert state(op, "call", [1.0], "grad_out") is op._ex
     op._ex = None
     with pytest.raises(cra.EpError, match="before any dispatch_standard_moe"):
         state(op, "call", Fields(device=torch.device("cuda:0")), "grad_out")
