@@ -897,10 +897,19 @@ class EpDispatchCombineOp:
         on the stream it was of."""
         if stream is None:
             return make(shape, dtype=dtype, device=self.workspace.device)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.workspace.device)
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(self._torch_stream(stream)):
             return make(shape, dtype=dtype, device=self.workspace.device)
+
+    def _torch_stream(self, stream):
+        """A call's stream (a torch stream or a hipStream_t) as torch's object.
+        Handle 0 is the default stream; torch's ExternalStream takes 0 for no
+        handle and makes a stream of its own, unordered with the call's."""
+        if isinstance(stream, torch.cuda.Stream):
+            return stream
+        handle, dev = int(stream), self.workspace.device
+        if handle == 0:
+            return torch.cuda.default_stream(dev)
+        return torch.cuda.ExternalStream(handle, device=dev)
 
     def _zeros(self, shape, dtype, stream):
         return self._new(shape, dtype, stream, torch.zeros)

@@ -1,0 +1,49 @@
+"""The streams of the op's layer methods on the GPU: the default stream by its
+handle."""
+import pytest
+import torch
+
+import combine_route_amd as cra
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    cra.load()
+
+
+def test_stream_handle_0_is_the_default_stream():
+    """Where a call on handle 0 makes its tensors: on the default stream, by
+    torch's own account; and the gradients of such a call are those of a call
+    on torch's current stream."""
+    op = cra.EpDispatchCombineOp(cra.make_config(2, 64, 8, 4, 2), with_weights=False,
+                                 expert_capacity=16)
+    seen = []
+
+    def make(shape, dtype, device):
+        seen.append(torch.cuda.current_stream(device).cuda_stream)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+    default = torch.cuda.default_stream().cuda_stream
+    assert default == 0
+    op._new((4,), torch.int32, default, make)
+    side = torch.cuda.Stream()
+    op._new((4,), torch.int32, side.cuda_stream, make)
+    op._new((4,), torch.int32, side, make)
+    assert seen == [default, side.cuda_stream, side.cuda_stream]
+    g = torch.Generator().manual_seed(0)
+    ids = torch.rand((2, 8, 8), generator=g).argsort(-1)[..., :2].to(torch.int32).cuda()
+    x = torch.randn((2, 8, 64), generator=g).to(torch.bfloat16).cuda()
+    px, _, _, _ = op.dispatch_standard_moe(x, None, None, ids)
+    y = torch.randn(px.shape, generator=g).to(torch.bfloat16).cuda()
+    w = torch.rand((2, 8, 2), generator=g).cuda()
+    want = op.combine_standard_moe_backward(x, w, ids, y)
+    got = op.combine_standard_moe_backward(x, w, ids, y, stream=default)
+    gx = op.dispatch_standard_moe_backward(want[0]), op.dispatch_standard_moe_backward(
+        want[0], stream=default)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(*gx)
