@@ -825,7 +825,12 @@ class EpDispatchCombineOp:
         (gate_up_scales [E, 2 I / 128, H / 128], down_scales [E, ceil(H / 128),
         I / 128]). Returns the experts' outputs [W, Er, cap, H] in the combine
         type, a view of a buffer the next call overwrites; rows past an
-        expert's count are not written."""
+        expert's count are not written. The hidden rows lie in the op's memory
+        too, so the whole of a call, not its result alone, has to come after
+        the call before it: as a plan's, calls on different streams (and
+        replays of graphs that hold one) are ordered by the caller. close()
+        waits for the last call; a graph that holds one is not replayed after
+        it."""
         cfg = self.cfg
         H, cap = cfg.hidden_dim, self.expert_capacity
         if (cfg.dispatch_dtype != EP_FP8_E4M3 or cfg.scale_type_size != 4 or
@@ -850,6 +855,9 @@ class EpDispatchCombineOp:
                            self._new((G, cap, inter // 128), torch.float32, stream),
                            self._new((W, Er, cap, H), _TORCH[cfg.combine_dtype], stream))
         hidden, hidden_scales, y = bufs[inter]
+        # what close() waits for: calls on several streams are in the caller's
+        # order, so the last one's end is the end of all
+        ex["mlp_stream"] = _stream(stream, self._dev_index)
         counts = packed_recv_count.view(G)
         moe_grouped_gemm_swiglu(rows.view(G, cap, H), scales.view(torch.float32).view(
             G, cap, H // 128), gate_up, gate_up_scales, hidden, hidden_scales, counts, stream)
@@ -928,7 +936,12 @@ class EpDispatchCombineOp:
         self._dcache = self._ccache = None
         if self._ex is not None:
             ex, self._ex = self._ex, None
-            ep_expert_plan_destroy(ex["plan"])
+            try:
+                # (destroying a plan waits for its own last stream alone)
+                if ex.get("mlp_stream") is not None:
+                    self._torch_stream(ex["mlp_stream"]).synchronize()
+            finally:
+                ep_expert_plan_destroy(ex["plan"])
         if self.plan:
             ep_plan_destroy(self.plan)
             self.plan = None

@@ -1,5 +1,5 @@
 """The streams of the op's layer methods on the GPU: the default stream by its
-handle."""
+handle, and what close() waits for."""
 import pytest
 import torch
 
@@ -47,3 +47,26 @@ def test_stream_handle_0_is_the_default_stream():
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.equal(*gx)
+
+
+def test_close_waits_for_expert_mlp_on_another_stream():
+    op = cra.EpDispatchCombineOp(cra.make_config(2, 256, 8, 2, 2, "fp8", "bf16", scale_dim=2),
+                                 with_weights=False, expert_capacity=16)
+    codes = torch.zeros((2, 8, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.ones((2, 8, 2), device="cuda")
+    ids = torch.tensor([0, 3], dtype=torch.int32, device="cuda").expand(2, 8, 2).contiguous()
+    px, count, _, _ = op.dispatch_standard_moe(codes, None, scales, ids)
+    up, ups = torch.zeros((4, 256, 256), dtype=torch.uint8, device="cuda"), torch.ones(
+        (4, 2, 2), device="cuda")
+    down, downs = torch.zeros((4, 256, 128), dtype=torch.uint8, device="cuda"), torch.ones(
+        (4, 2, 1), device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    y = op.expert_mlp(px, count, up, ups, down, downs, stream=side)
+    op.close()
+    assert side.query()
+    n = count.flatten().tolist()
+    for g, c in enumerate(n):
+        assert bool((y.view(4, 16, 256)[g, :c] == 0).all())

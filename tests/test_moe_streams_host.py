@@ -50,3 +50,58 @@ def test_stream_handle_0_is_the_default_stream(log):
     log.clear()
     op._new((3,), torch.float32, None)
     assert log == []
+
+
+def mlp_op(monkeypatch, log):
+    """An op whose products are stand-ins, over CPU memory."""
+    for name in ("moe_grouped_gemm_swiglu", "moe_grouped_gemm"):
+        monkeypatch.setattr(cra, name, lambda *a, name=name: log.append((name, a[-1])))
+    monkeypatch.setattr(cra, "ep_expert_plan_destroy", lambda plan: log.append(("destroy", plan)))
+    op = object.__new__(cra.EpDispatchCombineOp)
+    op.cfg = cra.make_config(2, 256, 4, 2, 2, "fp8", "bf16", scale_dim=2)
+    op.expert_capacity, op.plan, op._dev_index = 8, None, 0
+    op.workspace = Fields(device=CPU)
+    op._ex = {"plan": 7}
+    return op
+
+
+def mlp(op, inter=128, stream=None):
+    G, cap, H = 4, op.expert_capacity, 256
+    rows = torch.zeros((2, 2, cap, H), dtype=torch.uint8)
+    scales = torch.zeros((2, 2, cap, H // 128 * 4), dtype=torch.uint8)
+    up, down = torch.zeros((G, 2 * inter, H), dtype=torch.uint8), torch.zeros((G, H, inter),
+                                                                              dtype=torch.uint8)
+    return op.expert_mlp((rows, scales), torch.zeros((2, 2), dtype=torch.int32), up, None, down,
+                         None, stream=stream)
+
+
+@pytest.mark.parametrize("streams,last", [([0x10], 0x10), ([0x10, 0x20], 0x20), ([0x10, 0], "default")])
+def test_close_waits_for_the_last_expert_mlp(monkeypatch, log, streams, last):
+    """Destroying the plan waits for the plan's own last stream; the products
+    may be on another one, and their buffers go with the op."""
+    op = mlp_op(monkeypatch, log)
+    for s in streams:
+        mlp(op, stream=s)
+    log.clear()
+    op.close()
+    assert log == [("wait", last), ("destroy", 7)]
+
+
+def test_close_without_expert_mlp_waits_for_no_stream(monkeypatch, log):
+    op = mlp_op(monkeypatch, log)
+    op.close()
+    assert log == [("destroy", 7)]
+
+
+def test_close_frees_the_plan_when_the_wait_fails(monkeypatch, log):
+    op = mlp_op(monkeypatch, log)
+    mlp(op, stream=0x10)
+    log.clear()
+
+    def refused(handle, device=None):
+        raise RuntimeError("no such stream")
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", refused)
+    with pytest.raises(RuntimeError, match="no such stream"):
+        op.close()
+    assert log == [("destroy", 7)] and op._ex is None
