@@ -848,12 +848,14 @@ class EpDispatchCombineOp:
                              f"not {list(gate_up.shape)} and {list(down.shape)}")
         ex = self._expert_state()
         # buffers of each hidden size are kept until close(): a captured graph
-        # may hold them
+        # may hold them; the outputs' buffer serves every hidden size
         bufs = ex.setdefault("mlp", {})
         if inter not in bufs:
+            y = next((b[2] for b in bufs.values()), None)
+            if y is None:
+                y = self._new((W, Er, cap, H), _TORCH[cfg.combine_dtype], stream)
             bufs[inter] = (self._new((G, cap, inter), torch.uint8, stream),
-                           self._new((G, cap, inter // 128), torch.float32, stream),
-                           self._new((W, Er, cap, H), _TORCH[cfg.combine_dtype], stream))
+                           self._new((G, cap, inter // 128), torch.float32, stream), y)
         hidden, hidden_scales, y = bufs[inter]
         # what close() waits for: calls on several streams are in the caller's
         # order, so the last one's end is the end of all

@@ -1,5 +1,5 @@
 """The streams of the op's layer methods on the GPU: the default stream by its
-handle, and what close() waits for."""
+handle, what close() waits for, and two hidden sizes over one output buffer."""
 import pytest
 import torch
 
@@ -70,3 +70,51 @@ def test_close_waits_for_expert_mlp_on_another_stream():
     n = count.flatten().tolist()
     for g, c in enumerate(n):
         assert bool((y.view(4, 16, 256)[g, :c] == 0).all())
+
+
+def test_expert_mlp_of_two_hidden_sizes_in_turn():
+    """Two expert sizes share the outputs' buffer: each call's outputs are its
+    own, eager and as replays of one graph that holds both."""
+    op = cra.EpDispatchCombineOp(cra.make_config(2, 256, 8, 2, 2, "fp8", "bf16", scale_dim=2),
+                                 with_weights=False, expert_capacity=16)
+    g = torch.Generator().manual_seed(3)
+
+    def codes(*shape):
+        return torch.randint(0, 0x40, shape, generator=g, dtype=torch.uint8).cuda()
+
+    ids = torch.tensor([1, 2], dtype=torch.int32, device="cuda").expand(2, 8, 2).contiguous()
+    px, count, _, _ = op.dispatch_standard_moe(codes(2, 8, 256), None,
+                                               torch.ones((2, 8, 2), device="cuda"), ids)
+    experts = []
+    for inter in (128, 384):
+        experts.append((codes(4, 2 * inter, 256), torch.full((4, inter // 64, 2), 2.0 ** -8,
+                                                             device="cuda"),
+                        codes(4, 256, inter), torch.ones((4, 2, inter // 128), device="cuda")))
+
+    def outputs(y):
+        return torch.cat([y.view(4, 16, 256)[e, :c] for e, c in enumerate(rows)])
+
+    rows = count.flatten().tolist()
+    want = []
+    for e in experts:
+        y = op.expert_mlp(px, count, *e)
+        want.append(outputs(y).clone())
+    assert sum(rows) == 32 and not torch.equal(*want)
+    assert op.expert_mlp(px, count, *experts[0]).data_ptr() == y.data_ptr()
+    for e, w in zip(experts, want):
+        assert torch.equal(outputs(op.expert_mlp(px, count, *e)), w)
+    kept = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for e, k in zip(experts, kept):
+            k.copy_(outputs(op.expert_mlp(px, count, *e)))
+    for _ in range(3):
+        for k in kept:
+            k.zero_()
+        y.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, w in zip(kept, want):
+            assert torch.equal(k, w)

@@ -65,7 +65,7 @@ def mlp_op(monkeypatch, log):
     return op
 
 
-def mlp(op, inter=128, stream=None):
+def mlp(op, inter=128, stream=0x10):
     G, cap, H = 4, op.expert_capacity, 256
     rows = torch.zeros((2, 2, cap, H), dtype=torch.uint8)
     scales = torch.zeros((2, 2, cap, H // 128 * 4), dtype=torch.uint8)
@@ -105,3 +105,15 @@ def test_close_frees_the_plan_when_the_wait_fails(monkeypatch, log):
     with pytest.raises(RuntimeError, match="no such stream"):
         op.close()
     assert log == [("destroy", 7)] and op._ex is None
+
+
+def test_expert_mlp_has_one_output_buffer(monkeypatch, log):
+    """The experts' outputs do not depend on the hidden size: one buffer, for
+    every size that is used."""
+    op = mlp_op(monkeypatch, log)
+    y = mlp(op)
+    assert y.shape == (2, 2, 8, 256) and y.dtype == torch.bfloat16
+    for inter in (256, 384, 128):
+        assert mlp(op, inter).data_ptr() == y.data_ptr()
+    hidden = {b[0].shape[2]: b[0].data_ptr() for b in op._ex["mlp"].values()}
+    assert sorted(hidden) == [128, 256, 384] and len(set(hidden.values())) == 3
