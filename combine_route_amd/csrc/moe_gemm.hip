@@ -137,31 +137,39 @@ __device__ __forceinline__ void phase_end()
 // so, the only waits are this file's own. No register is written, so nothing
 // the load does later can meet the compiler's registers, and its own counted
 // waits only get stricter by loads it does not know of.
-// dst is an LDS address. M0 holds it; nothing else here uses M0. What is
-// checked against the resource's bytes is off + soff, whichever part of it is
-// past them (measured on gfx950, soff past them too).
+// dst is an LDS address. M0 holds it, and is named as overwritten: the
+// compiler keeps no value of its own there across the statement (it warns that
+// it would not hand the register out either). What is checked against the resource's
+// bytes is off + soff, whichever part of it is past them (measured on gfx950,
+// soff past them too).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <bool NT>
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off, uint32_t soff)
 {
     if constexpr (NT)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
                      ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
-                     : "memory");
+                     : "memory", "m0");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                      ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
-                     : "memory");
+                     : "memory", "m0");
 }
 
-// The same for lanes 0 to 31 alone. Every lane of the wave is active here.
+// The same for those of lanes 0 to 31 that are active; the mask is as before
+// afterwards.
 __device__ __forceinline__ void load_half_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off,
                                                  uint32_t soff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, 0xffffffff\n\t"
-                 "buffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_mov_b64 exec, -1"
-                 ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
-                 : "memory");
+    uint64_t lanes;
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, exec\n\ts_mov_b32 exec_hi, 0\n\t"
+                 "buffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b64 exec, %0"
+                 : "=&s"(lanes)
+                 : "s"(dst), "v"(off), "s"(rsrc), "s"(soff)
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // A base that every lane holds alike, and its row_rsrc, in scalar registers: a
 // resource the compiler takes for a lane's own costs a loop over the lanes at
