@@ -581,6 +581,21 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
     phase_end();
 }
 
+// exp(-g) to 4 half steps (2 of v_exp_f32, a rounding of each factor) wherever it
+// is normal: 2 to the power of -g log2(e), which one float holds only to |g| half
+// steps of the result, as t + r, and 2^(t + r) = 2^t (1 + r ln 2). r is no number
+// or anything where t is infinite or 2^t is 0 or infinite: held to [-1, 1] (a NaN
+// to -1), it changes neither.
+__device__ __forceinline__ float exp_minus(float g)
+{
+    constexpr double kLog2e = 1.4426950408889634;
+    constexpr float hi = (float)kLog2e, lo = (float)(kLog2e - (double)hi);
+    const float t = -g * hi;
+    const float r = __builtin_fmaf(-g, lo, __builtin_fmaf(-g, hi, -t));
+    return __builtin_amdgcn_exp2f(t) *
+           __builtin_fmaf(__builtin_amdgcn_fmed3f(r, -1.0f, 1.0f), 0.6931471805599453f, 1.0f);
+}
+
 // The tile's sums to memory.
 template <int TS, int DT, bool kSwiglu>
 __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (*s_amax)[tile_rows(TS)],
@@ -631,7 +646,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
                     const float g = acc[j][s][r];
                     // both sides of the quotient over 16, so that the reciprocal
                     // stays in the normal range wherever the exponential is finite
-                    const float d = __builtin_fmaf(__expf(-g), 0.0625f, 0.0625f);
+                    const float d = __builtin_fmaf(exp_minus(g), 0.0625f, 0.0625f);
                     const float z = g * 0.0625f * __builtin_amdgcn_rcpf(d) * acc[j][kGate + s][r];
                     acc[j][s][r] = z;
                     amax = __builtin_fmaxf(amax, __builtin_fabsf(z));
