@@ -11,13 +11,16 @@
 // few of 32 (swiglu form), 64, 128 or 224 rows as hold its rows, so that experts
 // with few rows cost their weights' bytes and little else.
 //
-// The FP8 matrix instruction adds 8 products at a time after aligning them to
-// the largest of the 8 and cutting what lies below 2^-13 of it (measured on
-// gfx950: 2^16 + 2^2 gives 2^16 among 8 neighbouring k, 2^16 + 2^-7 is kept
-// across them; the same in v_mfma_f32_16x16x32_fp8_fp8). Rows of bf16 / fp16
-// take it: its error, 1.3e-5 of a row's norm whatever k, is 1/20 of fp16's
-// rounding and 1/150 of bf16's. The swiglu form returns its block scales in
-// FP32 (off by 1.2e-5 that way), so there both operands are widened to fp16
+// The FP8 matrix instruction adds 8 products of neighbouring k at a time, each
+// first cut toward zero to a multiple of 2^(E - 13), E the largest sum of the
+// operands' exponents among the nonzero ones, a subnormal's taken as -6 (measured
+// on gfx950: this gives its every result over random codes of all ranges; between
+// eights nothing is cut, 200704 - 200704 + 2^-6 is 2^-6; the same in
+// v_mfma_f32_16x16x32_fp8_fp8). Rows of bf16 / fp16 take it at twice the 16-bit
+// rate: what is lost is under 7/512 of what half a step of the codes that set E
+// makes up, and in rows of ordinary spread 1.3e-5 of a row's norm whatever k, 1/20
+// of fp16's rounding and 1/150 of bf16's. The swiglu form returns its block scales
+// in FP32 (off by 1.2e-5 that way), so there both operands are widened to fp16
 // (exact) in registers and multiplied by v_mfma_f32_16x16x32_f16, whose sums
 // of such products are FP32's (scales off by 2e-7); the matrix rate is half.
 //
