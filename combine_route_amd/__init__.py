@@ -780,9 +780,16 @@ class EpDispatchCombineOp:
         _check("ep_dispatch_standard_moe", self._lib.ep_dispatch_standard_moe(
             ex["plan"], ctypes.byref(c[2]), _stream(stream, self._dev_index)))
         ex["ccache"] = None
+        ex["dispatch_id"] = ex.get("dispatch_id", 0) + 1
         px = ex["packed_x"] if ex["packed_scales"] is None else (ex["packed_x"],
                                                                   ex["packed_scales"])
         return px, ex["packed_count"], ex["packed_src_info"], ex["packed_layout_range"]
+
+    @property
+    def dispatch_id(self):
+        """Number of the last dispatch_standard_moe call (0: none yet), whose map
+        the backward calls use. (A graph's replays do not count.)"""
+        return (self._ex or {}).get("dispatch_id", 0)
 
     def combine_standard_moe(self, input, weights, indices, call_reset=False, stream=None,
                              input_scales=None):
@@ -868,15 +875,21 @@ class EpDispatchCombineOp:
         return y
 
     def combine_standard_moe_backward(self, grad_out, weights, indices, packed_y=None,
-                                      grad_packed_y=None, grad_weights=None, stream=None):
+                                      grad_packed_y=None, grad_weights=None, stream=None,
+                                      dispatch_id=None):
         """Gradient of combine_standard_moe for the last dispatch_standard_moe:
         grad_out [W, M, H] of its result; weights, indices and packed_y its
         weights, ids and input. Returns (grad_packed_y [W, Er, cap, H],
         grad_weights [W, M, k]); the second is None without packed_y, and only
         taken with weights. Rows of no kept pair and of tokens t >= T_r are
         left untouched. The results are the tensors given for them, or new
-        ones (zeros)."""
-        ex = self._fused_state("combine_standard_moe_backward", grad_out, "grad_out")
+        ones (zeros).
+        The op holds the last dispatch's map alone. Where another dispatch comes
+        before a backward (layers or micro-batches that all go forward first),
+        each needs an op of its own, or its dispatch again. dispatch_id: the op's
+        dispatch_id after the dispatch that this is the gradient of; the call
+        is refused (EP_ERR_STATE) if the op has dispatched since."""
+        ex = self._fused_state("combine_standard_moe_backward", grad_out, "grad_out", dispatch_id)
         cfg = self.cfg
         W, M, k = cfg.world_size, cfg.max_num_inp_token_per_rank, cfg.num_experts_per_token
         if grad_packed_y is None:
@@ -888,12 +901,15 @@ class EpDispatchCombineOp:
                              packed_y, grad_packed_y, grad_weights, stream)
         return grad_packed_y, grad_weights
 
-    def dispatch_standard_moe_backward(self, grad_packed_x, grad_x=None, stream=None):
+    def dispatch_standard_moe_backward(self, grad_packed_x, grad_x=None, stream=None,
+                                       dispatch_id=None):
         """Gradient of dispatch_standard_moe's rows: grad_x [W, M, H] from
         grad_packed_x [W, Er, cap, H], both in the combine type. Rows of
         tokens t >= T_r are left untouched. Returns the tensor given for it,
-        or a new one (zeros)."""
-        ex = self._fused_state("dispatch_standard_moe_backward", grad_packed_x, "grad_packed_x")
+        or a new one (zeros). dispatch_id, and layers that share an op, as
+        combine_standard_moe_backward."""
+        ex = self._fused_state("dispatch_standard_moe_backward", grad_packed_x, "grad_packed_x",
+                               dispatch_id)
         cfg = self.cfg
         if grad_x is None:
             grad_x = self._zeros((cfg.world_size, cfg.max_num_inp_token_per_rank, cfg.hidden_dim),
@@ -924,14 +940,17 @@ class EpDispatchCombineOp:
     def _zeros(self, shape, dtype, stream):
         return self._new(shape, dtype, stream, torch.zeros)
 
-    def _fused_state(self, call, given, name):
+    def _fused_state(self, call, given, name, dispatch_id=None):
         """The expert plan's state for a call on tensors that lie with `given`:
-        the plan's map is on the op's own device."""
+        the plan's map is on the op's own device, and of its last dispatch."""
         if self._ex is None:
             raise EpError(call, EP_ERR_STATE, f"{call} before any dispatch_standard_moe")
         # (what is no tensor is refused by the call itself)
         if getattr(given, "device", self.workspace.device) != self.workspace.device:
             raise ValueError(f"{name} is on {given.device}, the op on {self.workspace.device}")
+        if dispatch_id is not None and dispatch_id != self.dispatch_id:
+            raise EpError(call, EP_ERR_STATE, f"{call} of dispatch {dispatch_id}: the op holds the "
+                          f"map of dispatch {self.dispatch_id}")
         return self._ex
 
     def close(self):

@@ -149,7 +149,11 @@ int moe_grouped_gemm(const moe_grouped_gemm_args_t *args, void *stream);
  * Gradients of the fused calls. Both use the map of the last
  * ep_dispatch_standard_moe on the expert plan, as ep_combine_standard_moe
  * does (a later ep_convert_dispatch_output on the plan ends it); they may be
- * called any number of times per dispatch. Gradients are taken through the
+ * called any number of times per dispatch. The map is not kept past the next
+ * fused dispatch, and a call cannot tell whose it is: where other dispatches come
+ * between a dispatch and its gradient (layers or micro-batches that all go
+ * forward first), each needs an expert plan of its own, or its dispatch again
+ * before the gradient. Gradients are taken through the
  * calls' sums in FP32: the combine's rounding of each rank's part and of the
  * result count as the identity, and so does a dispatch_cast. W, M, k, Er, H
  * and cap are the plan's, rows have its combine_dtype (whatever its

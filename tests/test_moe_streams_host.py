@@ -117,3 +117,4 @@ def test_expert_mlp_has_one_output_buffer(monkeypatch, log):
         assert mlp(op, inter).data_ptr() == y.data_ptr()
     hidden = {b[0].shape[2]: b[0].data_ptr() for b in op._ex["mlp"].values()}
     assert sorted(hidden) == [128, 256, 384] and len(set(hidden.values())) == 3
+    op.close()
