@@ -43,16 +43,26 @@
 //
 // Measured on MI355X (a large FP8 library product: 2.6 PFLOP/s, bf16 1.35;
 // weights streamed to LDS alone: 7.0 TB/s): 32 experts x 1024 rows, n 7168, k
-// 2048 545 us (1.77 PFLOP/s), n 4096, k 7168 960 us (2.0); gate and up, n
-// 4096, k 7168, 32768 rows in all 1.6 to 1.8 ms (1.1 PFLOP/s in fp16
-// products; without its loads 1.4 ms). Large tiles are bound by the matrix
-// units' power and the sums beside them: without their loads they take 780 us
-// instead of 960. 256 experts x 32 rows, n 7168, k 2048 680 us (5.7 TB/s; 545
-// without its stores: 117 MB of scattered rows in a stream of reads), gate and
-// up of 32 experts x 32 rows 177 us (5.3 TB/s; its loads alone 143, its products
-// and conversions alone 145): bound by memory and the phases of a step that do
-// not run beside each other. Tried and no faster: widening by shifts and masks
-// instead of conversions (221 against 180 us), the wave halves taking turns at reading and multiplying (1108
+// 2048 520 to 590 us over boxes and row counts (1.6 to 1.85 PFLOP/s), n 4096, k
+// 7168 965 us (2.0); gate and up, n 4096, k 7168, 32768 rows in all 1.66 to 1.86 ms
+// (1.0 to 1.16 PFLOP/s in fp16 products; without its loads 1.4 ms). No unit is full
+// in large tiles (counters at the first case): matrix units busy 42% of the
+// cycles, vector issue 37%, LDS 23%, at 2.0 GHz; without their loads they take 780
+// us instead of 960, so what bounds them is the phases of a step that do not run
+// beside each other. 256 experts x 32 rows, n 7168, k 2048 650 to 690 us (5.7 TB/s;
+// 545 without its stores: 117 MB of scattered rows in a stream of reads), gate and
+// up of 32 experts x 32 rows 175 us (5.3 TB/s; its loads alone 143, its products
+// and conversions alone 145): bound by memory and those phases. Fewer tiles than
+// compute units leave the rest idle and a step its loads' latency: 27 experts x 4
+// rows, k 4608, n 256, gate and up, 35 us for 32 MB.
+//   The swiglu kernel has 47 registers a lane in scratch memory (the rows kernels
+// none): a loop over k touches one, on the branch of k below 512, but the code
+// between tiles reloads them, and a reload waits for every load before it, the next
+// tile's first slices among them. They are 21 MB of scratch memory over the grid,
+// written once a call and more (counters: 23.5 MB written at 32 x 32 rows for 2.2
+// MB of output).
+//   Tried and no faster: widening by shifts and masks instead of conversions (221
+// against 180 us), the wave halves taking turns at reading and multiplying (1108
 // against 1010 us), raised wave priority, a step's loads all in its first
 // products (980 against 950 us), products of 32 x 32 x 16 in the swiglu form
 // (2.0 ms: a product's 32 sums run in one piece), operands a step ahead in
@@ -826,7 +836,9 @@ moe_gemm_kernel(GemmArgs a)
         if (next >= 0) {
             t = read_tile(s_tile[slot]);
             if (tile_class<kSwiglu>(t.rows) == TS) {
-                // the next tile's loads run under this one's stores
+                // the next tile's loads run under this one's stores (in the
+                // swiglu form finish() waits for them: it reloads what it
+                // needs from scratch memory, and waits are in order)
                 const Loads<TS, kSwiglu> then(a, t, lds, lds0);
                 then.prologue();
                 loading = true;
