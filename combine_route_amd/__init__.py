@@ -883,7 +883,7 @@ class EpDispatchCombineOp:
         grad_weights [W, M, k]); the second is None without packed_y, and only
         taken with weights. Rows of no kept pair and of tokens t >= T_r are
         left untouched. The results are the tensors given for them, or new
-        ones (zeros).
+        ones (zeros, made and owned by torch's allocator on the call's stream).
         The op holds the last dispatch's map alone. Where another dispatch comes
         before a backward (layers or micro-batches that all go forward first),
         each needs an op of its own, or its dispatch again. dispatch_id: the op's
@@ -906,7 +906,7 @@ class EpDispatchCombineOp:
         """Gradient of dispatch_standard_moe's rows: grad_x [W, M, H] from
         grad_packed_x [W, Er, cap, H], both in the combine type. Rows of
         tokens t >= T_r are left untouched. Returns the tensor given for it,
-        or a new one (zeros). dispatch_id, and layers that share an op, as
+        or a new one (as there). dispatch_id, and layers that share an op, as
         combine_standard_moe_backward."""
         ex = self._fused_state("dispatch_standard_moe_backward", grad_packed_x, "grad_packed_x",
                                dispatch_id)

@@ -43,7 +43,7 @@
 //
 // Measured on MI355X (a large FP8 library product: 2.6 PFLOP/s, bf16 1.35;
 // weights streamed to LDS alone: 7.0 TB/s): 32 experts x 1024 rows, n 7168, k
-// 2048 520 to 590 us over boxes and row counts (1.6 to 1.85 PFLOP/s), n 4096, k
+// 2048 520 to 590 us over cards and row counts (1.6 to 1.85 PFLOP/s), n 4096, k
 // 7168 965 us (2.0); gate and up, n 4096, k 7168, 32768 rows in all 1.66 to 1.86 ms
 // (1.0 to 1.16 PFLOP/s in fp16 products; without its loads 1.4 ms). No unit is full
 // in large tiles (counters at the first case): matrix units busy 42% of the
