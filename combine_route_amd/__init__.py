@@ -977,3 +977,5 @@ class EpDispatchCombineOp:
 from .moe import (MOE_EPILOGUE_ROWS, MOE_EPILOGUE_SWIGLU, MOE_EXPORTED,  # noqa: E402
                   MOE_FP32, moe_combine_backward, moe_dispatch_backward, moe_grouped_gemm,
                   moe_grouped_gemm_swiglu, moe_rms_norm)
+from .block import (BLOCK_EXPORTED, MOE_INT8, moe_block_norm,  # noqa: E402
+                    moe_block_norm_backward, moe_block_norm_backward_workspace_bytes)

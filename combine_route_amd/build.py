@@ -13,7 +13,8 @@ LIB = os.path.join(PKG, "libcombine_route_amd.so")
 SOURCES = [os.path.join(PKG, "csrc", f)
            for f in ("ep_plan.cpp", "ep_kernels.hip", "ep_expert.hip", "ep_wire.hip",
                      "ep_standard.hip", "ep_probe.hip", "ep_static.hip", "moe_host.cpp",
-                     "moe_norm.hip", "moe_backward.hip", "moe_gemm.hip")]
+                     "moe_norm.hip", "moe_backward.hip", "moe_gemm.hip", "block_host.cpp",
+                     "block_norm.hip", "block_backward.hip")]
 ARCH = "gfx950"
 
 FLAGS = [

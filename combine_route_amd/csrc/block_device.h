@@ -1,0 +1,81 @@
+// Device helpers of the kernels of a whole MoE block.
+#pragma once
+
+#include "block_kernels.h"
+#include "moe_device.h"
+
+namespace block {
+namespace dev {
+
+using namespace ep::dev;
+using namespace moe::dev;
+using ep::kWave;
+
+// Largest of the wave's values as bit patterns: of magnitudes (sign clear)
+// the largest magnitude, a NaN above every number.
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v)
+{
+    auto step = [&](auto ctrl) {
+        const int i = (int)v;
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(i, i, decltype(ctrl)::value, 0xF,
+                                                                 0xF, true);
+        v = v > o ? v : o;
+    };
+    step(std::integral_constant<int, kDppXor1>());
+    step(std::integral_constant<int, kDppXor2>());
+    step(std::integral_constant<int, kDppHalfMirror>());
+    step(std::integral_constant<int, kDppMirror>());
+    uint32_t m = 0;
+#pragma unroll
+    for (int l = 0; l < kWave; l += 16) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)v, l);
+        m = m > o ? m : o;
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v)
+{
+    return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+}
+
+// Scale and its inverse factor of an INT8 row whose largest magnitude has
+// these bits. NaN and infinity stay in the scale (and give codes of 0).
+__device__ __forceinline__ void int8_scale(uint32_t amax_bits, float* scale, float* factor)
+{
+    const float amax = __builtin_bit_cast(float, amax_bits);
+    const float u = amax <= moe::kTinyAmax ? moe::kTinyAmax : amax;
+    *scale = amax_bits ? __fdiv_rn(u, 127.0f) : 1.0f;
+    *factor = __fdiv_rn(127.0f, u);
+}
+
+// 4 INT8 codes, one a byte in order: nearest whole number, ties to even, NaN
+// 0. The factor keeps |v| under 127.5.
+__device__ __forceinline__ uint32_t int8x4(float f0, float f1, float f2, float f3)
+{
+    auto code = [](float v) {
+        return (uint32_t)(int)__builtin_rintf(v == v ? v : 0.0f) & 0xFFu;
+    };
+    return code(f0) | code(f1) << 8 | code(f2) << 16 | code(f3) << 24;
+}
+
+// 8 weights from element e on. WT: 0 bf16, 1 fp16, 2 fp32.
+template <int WT>
+__device__ __forceinline__ void weights8(__amdgpu_buffer_rsrc_t r, int e, float (&w)[8])
+{
+    if constexpr (WT == 2) {
+        const u32x4 lo = bload16<0>(r, (uint32_t)e * 4u);
+        const u32x4 hi = bload16<0>(r, (uint32_t)e * 4u + 16u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t l = lo[i], u = hi[i];  // bit_cast reads a vector's element 0
+            w[i] = __builtin_bit_cast(float, l);
+            w[4 + i] = __builtin_bit_cast(float, u);
+        }
+    } else {
+        widen<WT>(bload16<0>(r, (uint32_t)e * 2u), w);
+    }
+}
+
+}  // namespace dev
+}  // namespace block

@@ -1,0 +1,306 @@
+// Host side of include/moe_block.h: argument checks, launch geometry and
+// launches of the kernels of a whole MoE block. As in ep_plan.cpp, every
+// precondition is checked before anything is enqueued and a failed check names
+// the argument.
+#include "moe_block.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include "block_kernels.h"
+#include "ep_static.h"
+
+namespace {
+
+constexpr size_t kPtrAlign = 16;
+// Bytes a call may move before its rows stream past the caches: the 256 MB
+// last-level cache of an MI355X.
+constexpr int64_t kKeepBytes = 256ll << 20;
+
+int fail(int code, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return ep::set_error(code, buf);
+}
+
+int ok() { return ep::set_error(EP_OK, ""); }
+
+struct Pointer {
+    const void* ptr;
+    const char* name;
+    size_t align;
+    bool required;
+};
+
+template <int N>
+int check_pointers(const Pointer (&p)[N])
+{
+    for (int i = 0; i < N; ++i) {
+        if (!p[i].ptr) {
+            if (p[i].required)
+                return fail(EP_ERR_NULL, "%s is NULL", p[i].name);
+            continue;
+        }
+        if (reinterpret_cast<uintptr_t>(p[i].ptr) % p[i].align)
+            return fail(EP_ERR_ALIGN, "%s = %p is not %zu-byte aligned", p[i].name, p[i].ptr,
+                        p[i].align);
+    }
+    return EP_OK;
+}
+
+// Checks that the two norm calls share.
+template <class A>
+int check_norm(const A* a)
+{
+    if (a->dtype != EP_BF16 && a->dtype != EP_FP16)
+        return fail(EP_ERR_ARG, "args.dtype = %d: must be EP_BF16 or EP_FP16", a->dtype);
+    if (a->weight_dtype != a->dtype && a->weight_dtype != MOE_FP32)
+        return fail(EP_ERR_ARG, "args.weight_dtype = %d: must be args.dtype or MOE_FP32",
+                    a->weight_dtype);
+    if (a->rows < 0)
+        return fail(EP_ERR_ARG, "args.rows = %lld: must be >= 0", (long long)a->rows);
+    if (a->hidden < 8 || a->hidden % 8)
+        return fail(EP_ERR_ARG, "args.hidden = %d: must be a positive multiple of 8", a->hidden);
+    if (a->hidden > block::kNormMaxHidden)
+        return fail(EP_ERR_SIZE, "args.hidden = %d: must be at most %d", a->hidden,
+                    block::kNormMaxHidden);
+    if (!(a->eps >= 0.0f) || std::isinf(a->eps))
+        return fail(EP_ERR_ARG, "args.eps = %g: must be finite and >= 0", (double)a->eps);
+    if (!std::isfinite(a->residual_scale))
+        return fail(EP_ERR_ARG, "args.residual_scale = %g: must be finite",
+                    (double)a->residual_scale);
+    if (a->row_counts && (a->group_rows < 1 || a->rows % a->group_rows))
+        return fail(EP_ERR_ARG, "args.group_rows = %lld: must be >= 1 and divide rows = %lld",
+                    (long long)a->group_rows, (long long)a->rows);
+    if (a->gate && a->gate_rows != 0 && (a->gate_rows < 0 || a->rows % a->gate_rows))
+        return fail(EP_ERR_ARG, "args.gate_rows = %lld: must be 0 or divide rows = %lld",
+                    (long long)a->gate_rows, (long long)a->rows);
+    return EP_OK;
+}
+
+int weight_type(int weight_dtype, int dtype)
+{
+    return weight_dtype == MOE_FP32 ? 2 : dtype == EP_BF16 ? 0 : 1;
+}
+
+// How the backward's rows lie on its blocks.
+struct BackwardShape {
+    int chunks, row_waves, group_blocks, block_groups, blocks;
+};
+
+// Chunks a wave: as few as let 8 waves hold the row, at most 4 (then up to 16
+// waves). Blocks: one a compute unit for rows of 5 waves and more, whose
+// sums take the registers of most of a unit; more of shorter rows.
+bool backward_shape(int64_t rows, int hidden, int64_t groups, BackwardShape* s)
+{
+    if (rows < 1 || groups < 1 || groups > rows || rows % groups || hidden < 8 || hidden % 8 ||
+        hidden > block::kNormMaxHidden)
+        return false;
+    const int chunks = (hidden + block::kNormChunk - 1) / block::kNormChunk;
+    s->chunks = chunks <= 8 ? 1 : chunks <= 16 ? 2 : 4;
+    s->row_waves = (chunks + s->chunks - 1) / s->chunks;
+    const int64_t target = 256 * std::max(1, 8 / s->row_waves);
+    if (groups >= target) {
+        s->group_blocks = 1;
+        const int64_t each = (groups + target - 1) / target;
+        if (each > INT32_MAX)
+            return false;
+        s->block_groups = (int)each;
+        s->blocks = (int)((groups + each - 1) / each);
+    } else {
+        s->group_blocks = (int)std::min<int64_t>(rows / groups, target / groups);
+        s->block_groups = 1;
+        s->blocks = (int)groups * s->group_blocks;
+    }
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_block_norm(const moe_block_norm_args_t* a, void* stream_ptr)
+{
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    int rc = check_norm(a);
+    if (rc != EP_OK)
+        return rc;
+    if ((a->codes == nullptr) != (a->scales == nullptr))
+        return fail(EP_ERR_ARG, "args.codes and args.scales must both be set or both NULL");
+    if (a->codes && a->codes_dtype != EP_FP8_E4M3 && a->codes_dtype != MOE_INT8)
+        return fail(EP_ERR_ARG, "args.codes_dtype = %d: must be EP_FP8_E4M3 or MOE_INT8",
+                    a->codes_dtype);
+    const bool fp8 = a->codes && a->codes_dtype == EP_FP8_E4M3;
+    if (fp8 && a->hidden % 128)
+        return fail(EP_ERR_ARG, "args.hidden = %d: FP8 codes need a multiple of 128", a->hidden);
+    if ((a->pre_weight == nullptr) != (!a->out && !a->codes))
+        return fail(EP_ERR_ARG, "args.pre_weight must be set iff args.out or args.codes is");
+    if (a->rows == 0)
+        return ok();
+    const Pointer ptrs[] = {{a->y, "args.y", kPtrAlign, true},
+                            {a->residual, "args.residual", kPtrAlign, true},
+                            {a->residual_out, "args.residual_out", kPtrAlign, true},
+                            {a->post_weight, "args.post_weight", kPtrAlign, false},
+                            {a->gate, "args.gate", kPtrAlign, false},
+                            {a->pre_weight, "args.pre_weight", kPtrAlign, false},
+                            {a->out, "args.out", kPtrAlign, false},
+                            {a->codes, "args.codes", kPtrAlign, false},
+                            {a->scales, "args.scales", 4, false},
+                            {a->row_counts, "args.row_counts", 4, false}};
+    rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+
+    block::NormArgs na;
+    na.y = static_cast<const uint8_t*>(a->y);
+    na.res = static_cast<const uint8_t*>(a->residual);
+    na.res_out = static_cast<uint8_t*>(a->residual_out);
+    na.post = static_cast<const uint8_t*>(a->post_weight);
+    na.gate = static_cast<const uint8_t*>(a->gate);
+    na.pre = static_cast<const uint8_t*>(a->pre_weight);
+    na.out = static_cast<uint8_t*>(a->out);
+    na.codes = static_cast<uint8_t*>(a->codes);
+    na.scales = reinterpret_cast<uint8_t*>(a->scales);
+    na.counts = a->row_counts;
+    na.rows = a->rows;
+    na.group_rows = a->row_counts ? a->group_rows : a->rows;
+    na.gate_rows = a->gate && a->gate_rows ? a->gate_rows : a->rows;
+    na.H = a->hidden;
+    na.kind = !a->codes ? block::kNoCodes : fp8 ? block::kFp8Codes : block::kInt8Codes;
+    na.res_scale = a->residual_scale;
+    na.eps = a->eps;
+    // Waves a row: as few as hold it, doubled while the call has fewer waves
+    // than the chip holds at 8 a SIMD and a wave has more than one chunk.
+    const int chunks = (a->hidden + block::kNormChunk - 1) / block::kNormChunk;
+    int waves = 1;
+    while (waves * block::kNormChunks < chunks)
+        waves *= 2;
+    while (waves < block::kNormMaxWaves && waves < chunks && a->rows * waves < 8192)
+        waves *= 2;
+    na.row_waves = waves;
+    na.chunks = (chunks + waves - 1) / waves;
+    // a launch's work-items must fit in 32 bits
+    if (a->rows > ((int64_t)UINT32_MAX - 1024) / (waves * ep::kWave))
+        return fail(EP_ERR_SIZE, "args.rows = %lld is too large for one launch",
+                    (long long)a->rows);
+    const int64_t row_bytes = (int64_t)a->hidden * (6 + (a->out ? 2 : 0) + (a->codes ? 1 : 0));
+    const hipError_t e = block::launch_norm(na, a->dtype == EP_BF16 ? 0 : 1,
+                                            weight_type(a->weight_dtype, a->dtype),
+                                            a->rows * row_bytes > kKeepBytes,
+                                            static_cast<hipStream_t>(stream_ptr));
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "block_norm launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+size_t moe_block_norm_backward_workspace_bytes(int64_t rows, int32_t hidden, int64_t groups)
+{
+    BackwardShape s;
+    if (!backward_shape(rows, hidden, groups, &s)) {
+        fail(EP_ERR_ARG,
+             "rows = %lld, hidden = %d, groups = %lld: groups must divide rows and hidden be a "
+             "multiple of 8 up to %d",
+             (long long)rows, hidden, (long long)groups, block::kNormMaxHidden);
+        return 0;
+    }
+    ok();
+    return (size_t)3 * s.blocks * hidden * sizeof(float);
+}
+
+int moe_block_norm_backward(const moe_block_norm_backward_args_t* a, void* stream_ptr)
+{
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    int rc = check_norm(a);
+    if (rc != EP_OK)
+        return rc;
+    if ((a->pre_weight == nullptr) != (a->grad_out == nullptr))
+        return fail(EP_ERR_ARG, "args.pre_weight and args.grad_out must both be set or both NULL");
+    if (!a->grad_out && !a->grad_h)
+        return fail(EP_ERR_NULL, "args.grad_h and args.grad_out are both NULL");
+    if (a->grad_post_weight && !a->post_weight)
+        return fail(EP_ERR_ARG, "args.grad_post_weight needs args.post_weight");
+    if (a->grad_gate && !a->gate)
+        return fail(EP_ERR_ARG, "args.grad_gate needs args.gate");
+    if (a->grad_pre_weight && !a->pre_weight)
+        return fail(EP_ERR_ARG, "args.grad_pre_weight needs args.pre_weight");
+    if (a->rows == 0)
+        return ok();
+    const bool sums = a->grad_post_weight || a->grad_gate || a->grad_pre_weight;
+    const Pointer ptrs[] = {{a->y, "args.y", kPtrAlign, true},
+                            {a->h, "args.h", kPtrAlign, a->grad_out != nullptr},
+                            {a->grad_h, "args.grad_h", kPtrAlign, false},
+                            {a->grad_out, "args.grad_out", kPtrAlign, false},
+                            {a->post_weight, "args.post_weight", kPtrAlign, false},
+                            {a->gate, "args.gate", kPtrAlign, false},
+                            {a->pre_weight, "args.pre_weight", kPtrAlign, false},
+                            {a->grad_y, "args.grad_y", kPtrAlign, true},
+                            {a->grad_residual, "args.grad_residual", kPtrAlign, false},
+                            {a->grad_post_weight, "args.grad_post_weight", kPtrAlign, false},
+                            {a->grad_gate, "args.grad_gate", kPtrAlign, false},
+                            {a->grad_pre_weight, "args.grad_pre_weight", kPtrAlign, false},
+                            {a->workspace, "args.workspace", kPtrAlign, sums},
+                            {a->row_counts, "args.row_counts", 4, false}};
+    rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+    const int64_t gates = a->gate && a->gate_rows ? a->rows / a->gate_rows : 1;
+    if (gates > 1 && a->row_counts && a->gate_rows != a->group_rows)
+        return fail(EP_ERR_ARG, "args.gate_rows = %lld must be args.group_rows = %lld with "
+                    "args.row_counts", (long long)a->gate_rows, (long long)a->group_rows);
+    const int64_t groups = gates > 1 ? gates : a->row_counts ? a->rows / a->group_rows : 1;
+    BackwardShape s;
+    if (!backward_shape(a->rows, a->hidden, groups, &s) || gates > INT32_MAX)
+        return fail(EP_ERR_SIZE, "args.rows = %lld is too large", (long long)a->rows);
+    const int64_t need = (int64_t)3 * s.blocks * a->hidden * (int64_t)sizeof(float);
+    if (sums && a->workspace_bytes < need)
+        return fail(EP_ERR_SIZE, "args.workspace_bytes = %lld: %lld are needed",
+                    (long long)a->workspace_bytes, (long long)need);
+
+    block::NormBackwardArgs na;
+    na.y = static_cast<const uint8_t*>(a->y);
+    na.h = static_cast<const uint8_t*>(a->h);
+    na.gh = static_cast<const uint8_t*>(a->grad_h);
+    na.go = static_cast<const uint8_t*>(a->grad_out);
+    na.post = static_cast<const uint8_t*>(a->post_weight);
+    na.gate = static_cast<const uint8_t*>(a->gate);
+    na.pre = static_cast<const uint8_t*>(a->pre_weight);
+    na.gy = static_cast<uint8_t*>(a->grad_y);
+    na.gres = static_cast<uint8_t*>(a->grad_residual);
+    na.gpost = a->grad_post_weight;
+    na.ggate = a->grad_gate;
+    na.gpre = a->grad_pre_weight;
+    na.part = static_cast<float*>(a->workspace);
+    na.counts = a->row_counts;
+    na.groups = groups;
+    na.group_rows = a->rows / groups;
+    na.group_blocks = s.group_blocks;
+    na.block_groups = s.block_groups;
+    na.blocks = s.blocks;
+    na.gates = (int)gates;
+    na.H = a->hidden;
+    na.row_waves = s.row_waves;
+    na.chunks = s.chunks;
+    na.res_scale = a->residual_scale;
+    na.eps = a->eps;
+    const int64_t row_bytes = (int64_t)a->hidden * 12;
+    const hipError_t e = block::launch_norm_backward(na, a->dtype == EP_BF16 ? 0 : 1,
+                                                     weight_type(a->weight_dtype, a->dtype),
+                                                     a->rows * row_bytes > kKeepBytes,
+                                                     static_cast<hipStream_t>(stream_ptr));
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "block_norm_backward launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,78 @@
+// Argument structs and launch entry points of the kernels of a whole MoE
+// block (include/moe_block.h). Internal; the host side is block_host.cpp.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ep_kernels.h"
+#include "moe_kernels.h"
+
+namespace block {
+
+// block_norm.hip: chunks of 512 elements, 16 bytes a lane; a wave keeps up to
+// kNormChunks of each of its rows in registers.
+constexpr int kNormChunk = moe::kNormChunk;
+constexpr int kNormChunks = 4;
+constexpr int kNormMaxWaves = 16;
+constexpr int kNormMaxHidden = kNormChunk * kNormChunks * kNormMaxWaves;
+
+enum { kNoCodes = 0, kFp8Codes = 1, kInt8Codes = 2 };
+
+struct NormArgs {
+    const uint8_t* y;
+    const uint8_t* res;
+    uint8_t* res_out;
+    const uint8_t* post;         // or null
+    const uint8_t* gate;         // or null
+    const uint8_t* pre;          // null without out and codes
+    uint8_t* out;                // or null
+    uint8_t* codes;              // or null
+    uint8_t* scales;
+    const int32_t* counts;       // or null
+    int64_t rows, group_rows;
+    int64_t gate_rows;           // rows a gate, `rows` for one gate
+    int32_t H;
+    int32_t row_waves;           // waves a row: a power of two up to kNormMaxWaves
+    int32_t chunks;              // chunks a wave, <= kNormChunks
+    int32_t kind;                // of the codes
+    float res_scale, eps;
+};
+
+// dtype, wtype: 0 bf16, 1 fp16 (wtype also 2: fp32).
+hipError_t launch_norm(const NormArgs& a, int dtype, int wtype, bool stream, hipStream_t s);
+
+// block_backward.hip. A block of row_waves waves walks rows of one group, or
+// whole groups, and holds the sums over its rows.
+constexpr int kBackChunks = 4;
+
+struct NormBackwardArgs {
+    const uint8_t* y;
+    const uint8_t* h;            // or null
+    const uint8_t* gh;           // or null
+    const uint8_t* go;           // or null
+    const uint8_t* post;         // or null
+    const uint8_t* gate;         // or null
+    const uint8_t* pre;          // null iff go is
+    uint8_t* gy;
+    uint8_t* gres;               // or null
+    float* gpost;                // or null
+    float* ggate;                // or null
+    float* gpre;                 // or null
+    float* part;                 // [3][blocks][H]: post, gate, pre
+    const int32_t* counts;       // or null
+    int64_t groups, group_rows;
+    int32_t group_blocks;        // blocks a group; 1 if a block walks several
+    int32_t block_groups;        // groups a block
+    int32_t blocks;
+    int32_t gates;               // gates: 1, or `groups`
+    int32_t H;
+    int32_t row_waves;
+    int32_t chunks;              // chunks a wave, <= kBackChunks
+    float res_scale, eps;
+};
+
+hipError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int wtype, bool stream,
+                                hipStream_t s);
+
+}  // namespace block

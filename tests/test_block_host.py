@@ -1,0 +1,154 @@
+"""Host-side checks of include/moe_block.h (no GPU needed, no kernel is
+launched): every function is exported, and every bad argument is refused with
+its code and a message that names it, before anything is enqueued. Pointers
+are fake addresses that are never dereferenced."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import combine_route_amd as cra
+from combine_route_amd import block, moe
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x7F1000000000             # 16-byte aligned device-looking address
+
+
+@pytest.fixture(scope="module")
+def fn():
+    if not os.path.exists(cra.LIB_PATH):
+        import combine_route_amd.build as b
+        b.build()
+    return block._fn
+
+
+def test_exports_every_declared_function(fn):
+    with open(os.path.join(ROOT, "include", "moe_block.h")) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    names = re.findall(r"\b(?:int|size_t) (moe_\w+)\s*\(", text)
+    assert sorted(names) == sorted(block.BLOCK_EXPORTED)
+    for n in names:
+        assert fn(n) is not None and hasattr(cra, n.replace("_ex", ""))
+
+
+NORM = dict(y=FAKE, residual=FAKE, residual_out=FAKE, post_weight=FAKE, gate=FAKE,
+            pre_weight=FAKE, out=FAKE, codes=FAKE, scales=FAKE, row_counts=FAKE, rows=64,
+            group_rows=16, gate_rows=16, hidden=256, dtype=cra.EP_BF16, weight_dtype=cra.EP_BF16,
+            codes_dtype=cra.EP_FP8_E4M3, residual_scale=1.0, eps=1e-6)
+
+COMMON = [
+    (dict(y=None), cra.EP_ERR_NULL, "args.y"),
+    (dict(y=FAKE + 8), cra.EP_ERR_ALIGN, "args.y"),
+    (dict(post_weight=FAKE + 4), cra.EP_ERR_ALIGN, "post_weight"),
+    (dict(gate=FAKE + 4), cra.EP_ERR_ALIGN, "gate"),
+    (dict(pre_weight=FAKE + 4), cra.EP_ERR_ALIGN, "pre_weight"),
+    (dict(row_counts=FAKE + 2), cra.EP_ERR_ALIGN, "row_counts"),
+    (dict(rows=-1), cra.EP_ERR_ARG, "rows"),
+    (dict(group_rows=0), cra.EP_ERR_ARG, "group_rows"),
+    (dict(group_rows=7), cra.EP_ERR_ARG, "group_rows"),
+    (dict(gate_rows=-1), cra.EP_ERR_ARG, "gate_rows"),
+    (dict(gate_rows=48), cra.EP_ERR_ARG, "gate_rows"),
+    (dict(hidden=0), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=12), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=32768 + 128), cra.EP_ERR_SIZE, "hidden"),
+    (dict(dtype=cra.EP_FP8_E4M3), cra.EP_ERR_ARG, "dtype"),
+    (dict(weight_dtype=cra.EP_FP16), cra.EP_ERR_ARG, "weight_dtype"),
+    (dict(eps=-1.0), cra.EP_ERR_ARG, "eps"),
+    (dict(eps=math.nan), cra.EP_ERR_ARG, "eps"),
+    (dict(eps=math.inf), cra.EP_ERR_ARG, "eps"),
+    (dict(residual_scale=math.nan), cra.EP_ERR_ARG, "residual_scale"),
+    (dict(residual_scale=math.inf), cra.EP_ERR_ARG, "residual_scale"),
+]
+
+
+@pytest.mark.parametrize("change,code,word", COMMON + [
+    (dict(residual=None), cra.EP_ERR_NULL, "residual"),
+    (dict(residual_out=None), cra.EP_ERR_NULL, "residual_out"),
+    (dict(pre_weight=None), cra.EP_ERR_ARG, "pre_weight"),
+    (dict(out=None, codes=None, scales=None), cra.EP_ERR_ARG, "pre_weight"),
+    (dict(codes=None), cra.EP_ERR_ARG, "scales"),
+    (dict(scales=None), cra.EP_ERR_ARG, "codes"),
+    (dict(codes_dtype=cra.EP_BF16), cra.EP_ERR_ARG, "codes_dtype"),
+    (dict(hidden=136), cra.EP_ERR_ARG, "multiple of 128"),
+    (dict(residual=FAKE + 2), cra.EP_ERR_ALIGN, "residual"),
+    (dict(residual_out=FAKE + 2), cra.EP_ERR_ALIGN, "residual_out"),
+    (dict(out=FAKE + 8), cra.EP_ERR_ALIGN, "out"),
+    (dict(codes=FAKE + 8), cra.EP_ERR_ALIGN, "codes"),
+    (dict(scales=FAKE + 2), cra.EP_ERR_ALIGN, "scales"),
+    (dict(rows=1 << 27, group_rows=1 << 20), cra.EP_ERR_SIZE, "rows"),
+])
+def test_block_norm_refuses(fn, change, code, word):
+    a = block.MoeBlockNormArgs(**dict(NORM, **change))
+    assert fn("moe_block_norm")(ctypes.byref(a), None) == code
+    assert word in cra.ep_last_error()
+
+
+BACKWARD = {k: v for k, v in NORM.items() if k not in (
+    "residual", "residual_out", "out", "codes", "scales", "codes_dtype")}
+BACKWARD.update(h=FAKE, grad_h=FAKE, grad_out=FAKE, grad_y=FAKE, grad_residual=FAKE,
+                grad_post_weight=FAKE, grad_gate=FAKE, grad_pre_weight=FAKE, workspace=FAKE,
+                workspace_bytes=1 << 40)
+
+
+@pytest.mark.parametrize("change,code,word", COMMON + [
+    (dict(h=None), cra.EP_ERR_NULL, "args.h"),
+    (dict(grad_y=None), cra.EP_ERR_NULL, "grad_y"),
+    (dict(workspace=None), cra.EP_ERR_NULL, "workspace"),
+    (dict(grad_out=None), cra.EP_ERR_ARG, "grad_out"),
+    (dict(pre_weight=None), cra.EP_ERR_ARG, "pre_weight"),
+    (dict(grad_h=None, grad_out=None, pre_weight=None, grad_pre_weight=None), cra.EP_ERR_NULL,
+     "grad_h"),
+    (dict(post_weight=None), cra.EP_ERR_ARG, "grad_post_weight"),
+    (dict(gate=None), cra.EP_ERR_ARG, "grad_gate"),
+    (dict(grad_out=None, pre_weight=None), cra.EP_ERR_ARG, "grad_pre_weight"),
+    (dict(gate_rows=8), cra.EP_ERR_ARG, "gate_rows"),
+    (dict(workspace_bytes=4 * 16 * 256 * 12 - 1), cra.EP_ERR_SIZE, "workspace_bytes"),
+] + [(dict({n: FAKE + 8}), cra.EP_ERR_ALIGN, n) for n in (
+    "h", "grad_h", "grad_out", "grad_y", "grad_residual", "grad_post_weight", "grad_gate",
+    "grad_pre_weight", "workspace")])
+def test_block_norm_backward_refuses(fn, change, code, word):
+    a = block.MoeBlockNormBackwardArgs(**dict(BACKWARD, **change))
+    assert fn("moe_block_norm_backward")(ctypes.byref(a), None) == code
+    assert word in cra.ep_last_error()
+
+
+def test_calls_without_rows_are_no_work(fn):
+    a = block.MoeBlockNormArgs(**dict(NORM, rows=0, y=None, residual=None))
+    assert fn("moe_block_norm")(ctypes.byref(a), None) == cra.EP_OK
+    a = block.MoeBlockNormBackwardArgs(**dict(BACKWARD, rows=0, y=None, workspace=None))
+    assert fn("moe_block_norm_backward")(ctypes.byref(a), None) == cra.EP_OK
+    assert cra.ep_last_error() == ""
+    for name in ("moe_block_norm", "moe_block_norm_backward"):
+        assert fn(name)(None, None) == cra.EP_ERR_NULL
+
+
+def test_backward_workspace_bytes(fn):
+    size = cra.moe_block_norm_backward_workspace_bytes
+    assert size(64, 256, 4) == 64 * 256 * 12
+    assert size(1, 8) == 8 * 12
+    # never more parts than rows, whole parts for each group
+    for rows, hidden, groups in ((16384, 7168, 8), (3000, 264, 3000), (5000, 32768, 1)):
+        n = size(rows, hidden, groups)
+        assert n % (12 * hidden) == 0 and n // (12 * hidden) <= rows
+    for bad in ((0, 256, 1), (4, 12, 1), (4, 40000, 1), (4, 256, 3), (4, 256, 0)):
+        with pytest.raises(cra.EpError):
+            size(*bad)
+
+
+def test_tensors_off_the_gpu_are_refused():
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    w = torch.ones(128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        cra.moe_block_norm(x, x, w, 1e-6, out=x)
+    with pytest.raises(TypeError, match="y must"):
+        cra.moe_block_norm([1.0], x, w, 1e-6)
+    with pytest.raises(ValueError, match="GPU"):
+        cra.moe_block_norm_backward(x, x, 1e-6, x, grad_out=x, pre_weight=w)
+
+
+def test_the_other_headers_are_as_they_were():
+    """moe.h's functions keep their own binding."""
+    assert not set(block.BLOCK_EXPORTED) & set(moe.MOE_EXPORTED)
