@@ -874,6 +874,53 @@ class EpDispatchCombineOp:
                          stream)
         return y
 
+    def expert_mlp_int8(self, packed_recv_x, packed_recv_count, gate_up, gate_up_scales, down,
+                        down_scales, stream=None):
+        """expert_mlp in 8-bit integers: two grouped INT8 products with the hidden
+        rows quantized to INT8 between them (through bf16). The config must
+        dispatch INT8 rows as bytes with one FP32 scale a row (dispatch_dtype
+        "fp8", scale_dim 1; moe_block_norm and moe_quantize_int8 make such rows,
+        given to the dispatch as uint8). gate_up [E, 2 I, H] holds each expert's I
+        gate rows, then its I up rows, down [E, H, I], both int8 with FP32 scales
+        per output channel (gate_up_scales [E, 2 I], down_scales [E, H]); H and I
+        multiples of 16. Returns the experts' outputs [W, Er, cap, H] in the
+        combine type, a view of a buffer the next call overwrites (the hidden
+        rows' too: the order of calls, and close(), as expert_mlp)."""
+        cfg = self.cfg
+        H, cap = cfg.hidden_dim, self.expert_capacity
+        if cfg.dispatch_dtype != EP_FP8_E4M3 or cfg.scale_type_size != 4 or cfg.scale_dim != 1:
+            raise ValueError("expert_mlp_int8 needs dispatch_dtype fp8 (bytes) with scale_dim 1, "
+                             "one float32 scale a row")
+        W, Er = cfg.world_size, cfg.num_experts_per_rank
+        G = W * Er
+        if gate_up.dim() != 3 or gate_up.shape[1] % 32:
+            raise ValueError("gate_up must be [E, 2 I, H] with I a multiple of 16, not "
+                             f"{list(gate_up.shape)}")
+        inter = gate_up.shape[1] // 2
+        if tuple(gate_up.shape) != (G, 2 * inter, H) or tuple(down.shape) != (G, H, inter):
+            raise ValueError(f"gate_up and down must be {[G, 2 * inter, H]} and {[G, H, inter]}, "
+                             f"not {list(gate_up.shape)} and {list(down.shape)}")
+        rows, scales = packed_recv_x
+        ex = self._expert_state()
+        bufs = ex.setdefault("mlp_int8", {})  # kept until close(), as expert_mlp's
+        if inter not in bufs:
+            y = next((b[3] for b in bufs.values()), None)
+            if y is None:
+                y = self._new((W, Er, cap, H), _TORCH[cfg.combine_dtype], stream)
+            bufs[inter] = (self._new((G, cap, inter), torch.bfloat16, stream),
+                           self._new((G, cap, inter), torch.int8, stream),
+                           self._new((G, cap), torch.float32, stream), y)
+        hidden, codes, hidden_scales, y = bufs[inter]
+        ex["mlp_stream"] = _stream(stream, self._dev_index)
+        counts = packed_recv_count.view(G)
+        moe_grouped_gemm_int8_swiglu(rows.view(torch.int8).view(G, cap, H),
+                                     scales.view(torch.float32).view(G, cap), gate_up,
+                                     gate_up_scales, hidden, counts, stream)
+        moe_quantize_int8(hidden, codes, hidden_scales, counts, stream)
+        moe_grouped_gemm_int8(codes, hidden_scales, down, down_scales, y.view(G, cap, H), counts,
+                              stream)
+        return y
+
     def combine_standard_moe_backward(self, grad_out, weights, indices, packed_y=None,
                                       grad_packed_y=None, grad_weights=None, stream=None,
                                       dispatch_id=None):
@@ -978,4 +1025,5 @@ from .moe import (MOE_EPILOGUE_ROWS, MOE_EPILOGUE_SWIGLU, MOE_EXPORTED,  # noqa:
                   MOE_FP32, moe_combine_backward, moe_dispatch_backward, moe_grouped_gemm,
                   moe_grouped_gemm_swiglu, moe_rms_norm)
 from .block import (BLOCK_EXPORTED, MOE_INT8, moe_block_norm,  # noqa: E402
-                    moe_block_norm_backward, moe_block_norm_backward_workspace_bytes)
+                    moe_block_norm_backward, moe_block_norm_backward_workspace_bytes,
+                    moe_grouped_gemm_int8, moe_grouped_gemm_int8_swiglu, moe_quantize_int8)

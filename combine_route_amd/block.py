@@ -10,11 +10,13 @@ from typing import Optional
 import torch
 
 from . import _F32, _I32, EP_ERR_ARG, EP_FP8_E4M3, EpError, _check, _stream, ep_last_error, load
-from .moe import _CODES, _DTYPE_CODE, MOE_FP32, _index_of, _ptr
+from .moe import (_CODES, _DTYPE_CODE, _ROWS, MOE_EPILOGUE_ROWS, MOE_EPILOGUE_SWIGLU, MOE_FP32,
+                  _index_of, _ptr)
 
 MOE_INT8 = 4
 BLOCK_EXPORTED = ("moe_block_norm", "moe_block_norm_backward",
-                  "moe_block_norm_backward_workspace_bytes")
+                  "moe_block_norm_backward_workspace_bytes", "moe_quantize_int8",
+                  "moe_grouped_gemm_int8")
 
 _INT8 = (torch.int8,)
 
@@ -38,6 +40,19 @@ class MoeBlockNormBackwardArgs(ctypes.Structure):
         [("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)])
 
 
+class MoeQuantizeInt8Args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("rows", "codes", "scales", "row_counts")] +
+                [("n_rows", ctypes.c_int64), ("group_rows", ctypes.c_int64),
+                 ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32)])
+
+
+class MoeGroupedGemmInt8Args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("a", "a_scales", "b", "b_scales", "counts",
+                                                "out")] +
+                [(n, ctypes.c_int32) for n in ("groups", "cap", "n", "k", "out_dtype",
+                                               "epilogue")])
+
+
 def _declare(lib):
     """The functions of include/moe_block.h by name, with their types."""
     V, P = ctypes.c_void_p, ctypes.POINTER
@@ -45,6 +60,8 @@ def _declare(lib):
     lib.moe_block_norm_backward.argtypes = [P(MoeBlockNormBackwardArgs), V]
     lib.moe_block_norm_backward_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32,
                                                             ctypes.c_int64]
+    lib.moe_quantize_int8.argtypes = [P(MoeQuantizeInt8Args), V]
+    lib.moe_grouped_gemm_int8.argtypes = [P(MoeGroupedGemmInt8Args), V]
     fns = {name: getattr(lib, name) for name in BLOCK_EXPORTED}
     for name, fn in fns.items():
         fn.restype = ctypes.c_size_t if name.endswith("_bytes") else ctypes.c_int
@@ -235,3 +252,60 @@ def moe_block_norm_backward(y: torch.Tensor, h: Optional[torch.Tensor], eps: flo
         None if ws is None else ws.data_ptr(), _ptr(counts, "counts", shape[:1], _I32, index),
         nbytes, rows, group, gate_rows, H, dtype, wt, residual_scale, eps)
     _call("moe_block_norm_backward", index, stream, a)
+
+
+def moe_quantize_int8(rows: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                      counts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_quantize_int8() (include/moe_block.h): rows [..., H] (bf16 or fp16) to
+    codes [..., H] (int8) and scales [...] (float32, one a row). counts: int32,
+    one count per leading index of rows; only the first counts[g] rows of group
+    g are read and written."""
+    index, shape, H, n_rows, dtype = _rows_of(rows, "rows")
+    _index_of(codes, "codes")
+    _index_of(scales, "scales")
+    group = _groups(counts, shape, n_rows)
+    a = MoeQuantizeInt8Args(
+        _ptr(rows, "rows", shape, (rows.dtype,), index), _ptr(codes, "codes", shape, _INT8, index),
+        _ptr(scales, "scales", shape[:-1], _F32, index),
+        _ptr(counts, "counts", shape[:1], _I32, index), n_rows, group, H, dtype)
+    _call("moe_quantize_int8", index, stream, a)
+
+
+def _product(a, a_scales, b, b_scales, out, counts, stream, epilogue):
+    index = _index_of(a, "a")
+    _index_of(b, "b")
+    _index_of(out, "out")
+    for t, name in ((a, "a"), (b, "b")):
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have 3 dimensions, not {t.dim()}")
+    groups, cap, k = a.shape
+    n = b.shape[1]
+    width = n // 2 if epilogue == MOE_EPILOGUE_SWIGLU else n
+    args = MoeGroupedGemmInt8Args(
+        _ptr(a, "a", a.shape, _INT8, index), _ptr(a_scales, "a_scales", (groups, cap), _F32, index),
+        _ptr(b, "b", (groups, n, k), _INT8, index),
+        _ptr(b_scales, "b_scales", (groups, n), _F32, index),
+        _ptr(counts, "counts", (groups,), _I32, index),
+        _ptr(out, "out", (groups, cap, width), _ROWS, index), groups, cap, n, k,
+        _DTYPE_CODE[out.dtype], epilogue)
+    _call("moe_grouped_gemm_int8", index, stream, args)
+
+
+def moe_grouped_gemm_int8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
+                          b_scales: torch.Tensor, out: torch.Tensor,
+                          counts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_grouped_gemm_int8() (include/moe_block.h) to bf16 / fp16 rows: a [G,
+    cap, K] int8 rows with a_scales [G, cap], b [G, N, K] int8 weights with
+    b_scales [G, N]; out [G, cap, N]. counts: int32 [G] rows of each group
+    (default: cap). Sums are exact, in 32-bit integers."""
+    _product(a, a_scales, b, b_scales, out, counts, stream, MOE_EPILOGUE_ROWS)
+
+
+def moe_grouped_gemm_int8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor,
+                                 b_scales: torch.Tensor, out: torch.Tensor,
+                                 counts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_grouped_gemm_int8() with MOE_EPILOGUE_SWIGLU: b [G, 2 I, K] holds each
+    expert's I gate rows, then its I up rows; out [G, cap, I] (bf16 or fp16)
+    gets silu(gate) * up, which moe_quantize_int8 makes the next product's rows
+    of."""
+    _product(a, a_scales, b, b_scales, out, counts, stream, MOE_EPILOGUE_SWIGLU)

@@ -1,0 +1,442 @@
+// gfx950 (MI355X, CDNA4) kernel of moe_grouped_gemm_int8
+// (include/moe_block.h): each expert's product of its expert-major INT8 rows
+// with its INT8 weights, summed exactly in 32-bit integers and scaled once an
+// element, to bf16 / fp16 rows or, with gate and up weights, to rows of
+// silu(gate) * up.
+//
+// A work item is a tile of up to 256 rows of one expert by 256 weight rows.
+// Row counts are on the GPU, so the launch is a fixed grid of one block a
+// compute unit; each block works out every expert's tile range from the
+// counts and walks its share of the tiles. An expert's last tile computes as
+// few of 64, 128, 192 or 256 rows as hold its rows, so that experts with few
+// rows cost their weights' bytes and little else.
+//
+// Inside a tile: 4 waves, one a SIMD, 2 along the rows x 2 along the weight
+// rows, each with up to 128 x 128 sums in registers: the fewest reads of LDS a
+// product (a wave of 128 x 64 would read 1.5 times as much, which with the
+// loads' writes is all that LDS can do while the matrix units are busy). For
+// each 64 elements of k (a step) the block holds both operands' slices in LDS,
+// loaded there directly from memory several steps before; a wave reads a
+// step's operands to registers during the step before, between the products.
+// One barrier a step: it says that the next step's slices are there and that
+// this step's, now in registers, may be overwritten.
+//
+// LDS slices are 64 bytes a row without padding; the four 16-byte chunks of a
+// row are permuted by a key of the row, so that any 8 rows a matrix operand
+// reads one after the other fall in different banks. The matrix instruction,
+// v_mfma_i32_32x32x32_i8, has the weights as its rows and the token rows as
+// its columns; which weight row is which of its rows is chosen so that a lane
+// ends up with runs of 8 consecutive columns of one token row.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "block_lds.h"
+
+namespace block {
+namespace {
+
+using namespace block::dev;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kThreads = 256;
+constexpr int kTileN = 256;   // weight rows a tile
+constexpr int kStep = 64;     // bytes of k a step
+constexpr int kSubs = 4;      // operands of 32 weight rows a wave
+constexpr int kMaxTS = 4;     // a tile of class TS has 64 TS rows
+constexpr int kTileRows = 64 * kMaxTS;
+constexpr int kBLoads = 4;    // 16-byte loads a lane and step, of weights
+
+constexpr int a_bytes(int ts) { return 64 * ts * kStep; }
+constexpr int stage_bytes(int ts) { return a_bytes(ts) + kTileN * kStep; }
+// Slices held: as many as fit.
+constexpr int stages(int ts) { return ts == 4 ? 4 : ts == 3 ? 5 : ts == 2 ? 6 : 7; }
+constexpr int kScaleBytes = (kTileRows + kTileN) * 4;
+constexpr int kScales = 144 * 1024;  // their place
+static_assert(stages(4) * stage_bytes(4) <= kScales && stages(3) * stage_bytes(3) <= kScales &&
+                  stages(2) * stage_bytes(2) <= kScales && stages(1) * stage_bytes(1) <= kScales,
+              "LDS of a block");
+constexpr int kLdsBytes = kScales + 2 * kScaleBytes;
+
+// One tile: the group's first row, how many rows, and the column tile.
+struct Tile {
+    int64_t row0;   // first row (of [groups * cap])
+    int group;
+    int rows;       // rows of the tile that exist, 1 .. kTileRows; 0: no tile
+    int col;        // column tile
+};
+
+// The loads of a tile. Wave w's i-th 1 KB of a slice holds rows 16 * (4 * i +
+// w) .. + 15, a lane one 16-byte chunk of a row. Chunks past k are asked for
+// too, from beyond the resource's end (zeros, without memory traffic), so that
+// every step has the same loads in flight and no branch.
+// kSwiglu: weight rows [0, 128) of the tile are gate rows 128 * col .., rows
+// [128, 256) the up rows. Otherwise they are rows 256 * col .. .
+template <int TS, bool kSwiglu>
+struct Loads {
+    static constexpr int kAll = TS + kBLoads;  // a wave and step
+    u32x4 ra, rb0, rb1;                        // rows, the two halves of the weights
+    u32x4 ras, rbs;                            // the rows' scales, this wave's weight rows'
+    uint32_t aoff, boff;
+    int aleft, bleft;                          // bytes of k from this lane's chunk on
+    uint32_t step64;                           // bytes of 64 rows of k
+    uint32_t lds0;
+    int wave;
+
+    __device__ __forceinline__ Loads(const GemmArgs& a, const Tile& t, uint32_t block_lds0)
+        : lds0(block_lds0)
+    {
+        const int lane = threadIdx.x & (kWave - 1);
+        wave = uniform(threadIdx.x / kWave);
+        const uint32_t K = (uint32_t)a.k;
+        const int lr = wave * 16 + (lane >> 2);  // row of i = 0; i adds 64
+        step64 = 64 * K;
+        const int achunk = (lane & 3) ^ ((lr >> 1) & 3);
+        const int bchunk = (lane & 3) ^ (((lr >> 1) & 1) | (((lr >> 3) & 1) << 1));
+        aoff = (uint32_t)lr * K + (uint32_t)achunk * 16u;
+        boff = (uint32_t)lr * K + (uint32_t)bchunk * 16u;
+        aleft = a.k - achunk * 16;
+        bleft = a.k - bchunk * 16;
+        ra = rsrc_words(a.a + t.row0 * K, t.rows * (int)K);
+        const int64_t first = (int64_t)t.group * a.n;
+        const int half = kSwiglu ? a.n / 2 : a.n;   // rows of one projection
+        const int r0 = t.col * (kSwiglu ? 128 : kTileN);
+        const int r1 = kSwiglu ? half + r0 : min(r0 + 128, a.n - 1);
+        const int n0 = min(128, half - r0);
+        const int n1 = kSwiglu ? n0 : max(0, min(128, a.n - r0 - 128));
+        rb0 = rsrc_words(a.b + (first + r0) * K, n0 * (int)K);
+        rb1 = rsrc_words(a.b + (first + r1) * K, n1 * (int)K);
+        ras = rsrc_words(a.as + t.row0, t.rows * 4);
+        rbs = wave < 2 ? rsrc_words(a.bs + first + r0, n0 * 4)
+                       : rsrc_words(a.bs + first + r1, n1 * 4);
+    }
+
+    __device__ __forceinline__ void row_load(int i, int h, int stage) const
+    {
+        const uint32_t past = h * kStep < aleft ? 0u : 1u << 30;
+        load_to_lds<false>(ra, lds0 + stage * stage_bytes(TS) + i * 4096 + wave * 1024,
+                           aoff + i * step64 + past, (uint32_t)h * kStep);
+    }
+
+    __device__ __forceinline__ void weight_load(int i, int h, int stage) const
+    {
+        const uint32_t past = h * kStep < bleft ? 0u : 1u << 30;
+        load_to_lds<(TS < kMaxTS)>(i < 2 ? rb0 : rb1,
+                    lds0 + stage * stage_bytes(TS) + a_bytes(TS) + i * 4096 + wave * 1024,
+                    boff + (i & 1) * step64 + past, (uint32_t)h * kStep);
+    }
+
+    // Load i of step h's.
+    __device__ __forceinline__ void load(int i, int h, int stage) const
+    {
+        if (i < TS)
+            row_load(i, h, stage);
+        else
+            weight_load(i - TS, h, stage);
+    }
+
+    // The scales (to block `which` of them) and the first slices.
+    __device__ __forceinline__ void prologue(int which) const
+    {
+        const uint32_t lane4 = (threadIdx.x & (kWave - 1)) * 4u;
+        const uint32_t at = lds0 + kScales + which * kScaleBytes + wave * 256;
+        load4_to_lds(ras, at, wave * 256 + lane4);
+        load4_to_lds(rbs, at + kTileRows * 4, (wave & 1) * 256 + lane4);
+#pragma unroll
+        for (int h = 0; h < stages(TS); ++h)
+#pragma unroll
+            for (int i = 0; i < kAll; ++i)
+                load(i, h, h);
+    }
+};
+
+// A wave's operands of one step.
+template <int TS>
+struct Operands {
+    i32x4 w[kSubs][2], t[TS][2];
+};
+
+// The sums of one tile, whose first slices are on their way.
+template <int TS, bool kSwiglu>
+__device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uint8_t* lds, int nk,
+                                         i32x16 (&acc)[TS][kSubs])
+{
+    using L = Loads<TS, kSwiglu>;
+    constexpr int S = stages(TS);
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wm = ld.wave >> 1, wn = ld.wave & 1;
+    const int q = lane >> 5, i32 = lane & 31;
+    // the weight row that is row i32 of an operand: runs of 8 for a lane of
+    // the result, which holds rows 8 b + 4 q + t, b and t 0 .. 3
+    const int b = i32 >> 3, j = (b >> 1) * 16 + ((i32 >> 2) & 1) * 8 + (b & 1) * 4 + (i32 & 3);
+    const int wkey = ((j >> 1) & 1) | (((j >> 3) & 1) << 1);
+    const int wrow = wn * (kSwiglu ? 64 : 128) + j;
+    const uint32_t wat = a_bytes(TS) + (uint32_t)wrow * kStep + (uint32_t)((q ^ wkey) * 16);
+    const int trow = wm * 32 * TS + i32;
+    const uint32_t tat = (uint32_t)trow * kStep + (uint32_t)((q ^ ((trow >> 1) & 3)) * 16);
+    auto sub = [](int s) { return (uint32_t)(kSwiglu ? (s >> 1) * 128 + (s & 1) * 32 : s * 32) * kStep; };
+
+    Operands<TS> op[2];
+    // operand i of the step in `stage`, weights and rows of the first half first
+    auto fetch = [&](Operands<TS>& o, int i, int stage) {
+        const uint8_t* base = lds + stage * stage_bytes(TS);
+        const int half = i / (kSubs + TS), k = i % (kSubs + TS);
+        if (k < kSubs)
+            o.w[k][half] = *reinterpret_cast<const i32x4*>(base + (half ? wat ^ 32 : wat) + sub(k));
+        else
+            o.t[k - kSubs][half] = *reinterpret_cast<const i32x4*>(
+                base + (half ? tat ^ 32 : tat) + (k - kSubs) * 32 * kStep);
+    };
+    constexpr int kFetches = 2 * (kSubs + TS);
+    constexpr int kProducts = 2 * kSubs * TS;
+
+    phase_end<(S - 1) * L::kAll>();
+#pragma unroll
+    for (int i = 0; i < kFetches; ++i)
+        fetch(op[0], i, 0);
+#pragma unroll
+    for (int m = 0; m < TS; ++m)
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s)
+            acc[m][s] = i32x16{};
+
+    int stage = 0;
+    auto step = [&](int h, Operands<TS>& now, Operands<TS>& then) {
+        phase_end<(S - 2) * L::kAll>();
+        const int next = stage + 1 == S ? 0 : stage + 1;
+#pragma unroll
+        for (int p = 0; p < kProducts; ++p) {
+            const int half = p / (kSubs * TS), m = p / kSubs % TS, s = p % kSubs;
+            acc[m][s] = __builtin_amdgcn_mfma_i32_32x32x32_i8(now.w[s][half], now.t[m][half],
+                                                              acc[m][s], 0, 0, 0);
+            // its share of the next step's operands, in the first half of the
+            // products, and of the loads
+#pragma unroll
+            for (int i = 2 * p * kFetches / kProducts;
+                 i < 2 * (p + 1) * kFetches / kProducts && i < kFetches; ++i)
+                fetch(then, i, next);
+#pragma unroll
+            for (int i = p * L::kAll / kProducts; i < (p + 1) * L::kAll / kProducts; ++i)
+                ld.load(i, h + S, stage);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        stage = next;
+    };
+    for (int h = 0; h < nk; h += 2) {
+        step(h, op[0], op[1]);
+        step(h + 1, op[1], op[0]);
+    }
+    phase_end();
+}
+
+// The tile's sums to memory.
+template <int TS, int DT, bool kSwiglu>
+__device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, const uint8_t* scales,
+                                       i32x16 (&acc)[TS][kSubs])
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave);
+    const int wm = wave >> 1, wn = wave & 1, q = lane >> 5;
+    const float* as = reinterpret_cast<const float*>(scales);
+    const float* bs = as + kTileRows;
+    const int width = kSwiglu ? a.n / 2 : a.n;
+    const int trow = wm * 32 * TS + (lane & 31);
+    const __amdgpu_buffer_rsrc_t ro =
+        uniform_rsrc(a.out + t.row0 * width * 2, (int64_t)t.rows * width * 2);
+    constexpr int kCols = kSwiglu ? kSubs / 2 : kSubs;
+    const int wcol = wn * kCols * 32;
+#pragma unroll
+    for (int s = 0; s < kCols; ++s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // runs of 8 columns
+            const int j = wcol + s * 32 + h * 16 + q * 8;       // in the tile
+            const int col = t.col * (kSwiglu ? 128 : kTileN) + j;
+            float cs[8], us[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                cs[r] = bs[j + r];
+                us[r] = kSwiglu ? bs[128 + j + r] : 0.0f;
+            }
+#pragma unroll
+            for (int m = 0; m < TS; ++m) {
+                const int row = trow + m * 32;
+                const float sa = as[row];
+                float f[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    f[r] = sa * (cs[r] * (float)acc[m][s][h * 8 + r]);
+                    if constexpr (kSwiglu)
+                        f[r] = silu_times(f[r], sa * (us[r] * (float)acc[m][s + kCols][h * 8 + r]));
+                }
+                if (col < width)  // rows past the tile's are dropped by the resource
+                    bstore16<0>(narrow<DT>(f), ro,
+                                ((uint32_t)row * (uint32_t)width + (uint32_t)col) * 2u);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ int tile_class(int rows) { return (rows + 63) / 64; }
+
+template <int DT, bool kSwiglu>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void
+block_gemm_kernel(GemmArgs a)
+{
+    __shared__ __align__(1024) uint8_t lds[kLdsBytes];
+    __shared__ int s_part[kThreads / kWave];
+    __shared__ int s_first[kThreads + 1];
+    __shared__ int s_tile[2][4];
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave);
+
+    // Row tiles of each thread's share of the groups, as where they start in
+    // the list of all (group after group).
+    auto rows_of = [&](int g) {
+        return a.counts ? max(0, min(a.counts[g], a.cap)) : a.cap;
+    };
+    const int share = (a.groups + kThreads - 1) / kThreads;
+    {
+        const int g0 = min(a.groups, (int)threadIdx.x * share), g1 = min(a.groups, g0 + share);
+        int mine = 0;
+        for (int g = g0; g < g1; ++g)
+            mine += (rows_of(g) + kTileRows - 1) / kTileRows;
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int u = __shfl_up(inc, o);
+            if (lane >= o)
+                inc += u;
+        }
+        if (lane == kWave - 1)
+            s_part[wave] = inc;
+        __syncthreads();
+        int before = inc - mine, total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / kWave; ++w) {
+            before += w < wave ? s_part[w] : 0;
+            total += s_part[w];
+        }
+        s_first[threadIdx.x] = before;
+        if (threadIdx.x == 0)
+            s_first[kThreads] = total;
+        __syncthreads();
+    }
+    const int64_t tiles = (int64_t)uniform(s_first[kThreads]) * a.col_tiles;
+
+    // Tiles in rounds of the grid; in a round each of the 8 XCDs (blocks are
+    // dealt to them in turn) takes consecutive tiles, which share weights and
+    // rows in its L2. A group's tiles are numbered rows first. Only the last
+    // round can leave a block without a tile.
+    auto tile_at = [&](int64_t t0) -> int64_t {
+        const int64_t left = tiles - t0;
+        if (left <= 0)
+            return -1;
+        const int here = (int)min((int64_t)gridDim.x, left);
+        const int each = (here + 7) / 8;
+        const int slot = (int)blockIdx.x / 8, place = ((int)blockIdx.x & 7) * each + slot;
+        return slot < each && place < here ? t0 + place : -1;
+    };
+    // The thread whose share holds the tile says which it is.
+    auto look_up = [&](int64_t tile, int (&info)[4]) {
+        const int u = (int)(tile / a.col_tiles);
+        int base = s_first[threadIdx.x];
+        if (u < base || u >= s_first[threadIdx.x + 1])
+            return;
+        int g = (int)threadIdx.x * share, rows = rows_of(g), n = (rows + kTileRows - 1) / kTileRows;
+        while (u >= base + n) {
+            base += n;
+            ++g;
+            rows = rows_of(g);
+            n = (rows + kTileRows - 1) / kTileRows;
+        }
+        const int at = (int)(tile - (int64_t)base * a.col_tiles);
+        info[0] = g;
+        info[1] = rows;
+        info[2] = at % n;
+        info[3] = at / n;
+    };
+    auto read_tile = [&](const int (&info)[4]) {
+        Tile t;
+        t.group = uniform(info[0]);
+        const int m = uniform(info[2]);
+        t.rows = min(kTileRows, uniform(info[1]) - m * kTileRows);
+        t.col = uniform(info[3]);
+        t.row0 = (int64_t)t.group * a.cap + m * kTileRows;
+        return t;
+    };
+
+    int64_t t0 = 0;
+    const int64_t tile = tile_at(t0);
+    if (tile < 0)
+        return;  // the whole block
+    look_up(tile, s_tile[0]);
+    __syncthreads();
+    Tile t = read_tile(s_tile[0]);
+    const int nk = ((a.k + kStep - 1) / kStep + 1) & ~1;  // steps, in pairs
+    bool loading = false;  // t's first slices are on their way
+    int slot = 0;          // of the tile and its scales
+    // One tile of class TS; then t is the next one (or has no rows).
+    auto run = [&](auto ts) {
+        constexpr int TS = decltype(ts)::value;
+        const Loads<TS, kSwiglu> ld(a, t, lds0);
+        if (!loading) {
+            // loads past the end of a tile of another class may still write
+            phase_end<0>();
+            ld.prologue(slot);
+        }
+        t0 += gridDim.x;
+        const int64_t next = tile_at(t0);
+        if (next >= 0)
+            look_up(next, s_tile[slot ^ 1]);  // read after the steps' barriers
+        i32x16 acc[TS][kSubs];
+        multiply<TS, kSwiglu>(ld, lds, nk, acc);
+        const Tile done = t;
+        const uint8_t* scales = lds + kScales + slot * kScaleBytes;
+        slot ^= 1;
+        t.rows = 0;
+        loading = false;
+        if (next >= 0) {
+            t = read_tile(s_tile[slot]);
+            if (tile_class(t.rows) == TS) {
+                // the next tile's loads run under this one's stores
+                const Loads<TS, kSwiglu> then(a, t, lds0);
+                then.prologue(slot);
+                loading = true;
+            }
+        }
+        finish<TS, DT, kSwiglu>(a, done, scales, acc);
+    };
+    while (t.rows > 0) {
+        switch (tile_class(t.rows)) {
+        case 4: run(std::integral_constant<int, 4>()); break;
+        case 3: run(std::integral_constant<int, 3>()); break;
+        case 2: run(std::integral_constant<int, 2>()); break;
+        default: run(std::integral_constant<int, 1>()); break;
+        }
+    }
+    phase_end<0>();  // no load may write LDS after the block's end
+}
+
+}  // namespace
+
+hipError_t launch_gemm(const GemmArgs& a, int dtype, bool swiglu, int blocks, hipStream_t s)
+{
+    const dim3 grid(blocks), block(kThreads);
+    if (swiglu) {
+        if (dtype == 0)
+            hipLaunchKernelGGL((block_gemm_kernel<0, true>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((block_gemm_kernel<1, true>), grid, block, 0, s, a);
+    } else if (dtype == 0) {
+        hipLaunchKernelGGL((block_gemm_kernel<0, false>), grid, block, 0, s, a);
+    } else {
+        hipLaunchKernelGGL((block_gemm_kernel<1, false>), grid, block, 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace block

@@ -92,6 +92,9 @@ int weight_type(int weight_dtype, int dtype)
     return weight_dtype == MOE_FP32 ? 2 : dtype == EP_BF16 ? 0 : 1;
 }
 
+// Blocks of a grouped product: one a compute unit of an MI355X.
+constexpr int kGemmBlocks = 256;
+
 // How the backward's rows lie on its blocks.
 struct BackwardShape {
     int chunks, row_waves, group_blocks, block_groups, blocks;
@@ -300,6 +303,113 @@ int moe_block_norm_backward(const moe_block_norm_backward_args_t* a, void* strea
                                                      static_cast<hipStream_t>(stream_ptr));
     if (e != hipSuccess)
         return fail(EP_ERR_HIP, "block_norm_backward launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int moe_quantize_int8(const moe_quantize_int8_args_t* a, void* stream_ptr)
+{
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    if (a->dtype != EP_BF16 && a->dtype != EP_FP16)
+        return fail(EP_ERR_ARG, "args.dtype = %d: must be EP_BF16 or EP_FP16", a->dtype);
+    if (a->n_rows < 0)
+        return fail(EP_ERR_ARG, "args.n_rows = %lld: must be >= 0", (long long)a->n_rows);
+    if (a->hidden < 8 || a->hidden % 8)
+        return fail(EP_ERR_ARG, "args.hidden = %d: must be a positive multiple of 8", a->hidden);
+    if (a->hidden > block::kQuantMaxHidden)
+        return fail(EP_ERR_SIZE, "args.hidden = %d: must be at most %d", a->hidden,
+                    block::kQuantMaxHidden);
+    if (a->row_counts && (a->group_rows < 1 || a->n_rows % a->group_rows))
+        return fail(EP_ERR_ARG, "args.group_rows = %lld: must be >= 1 and divide n_rows = %lld",
+                    (long long)a->group_rows, (long long)a->n_rows);
+    if (a->n_rows == 0)
+        return ok();
+    const Pointer ptrs[] = {{a->rows, "args.rows", kPtrAlign, true},
+                            {a->codes, "args.codes", kPtrAlign, true},
+                            {a->scales, "args.scales", 4, true},
+                            {a->row_counts, "args.row_counts", 4, false}};
+    const int rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+    block::QuantizeArgs qa;
+    qa.rows = static_cast<const uint8_t*>(a->rows);
+    qa.codes = static_cast<uint8_t*>(a->codes);
+    qa.scales = a->scales;
+    qa.counts = a->row_counts;
+    qa.n_rows = a->n_rows;
+    qa.group_rows = a->row_counts ? a->group_rows : a->n_rows;
+    qa.H = a->hidden;
+    // waves a row: as moe_block_norm's
+    const int chunks = (a->hidden + block::kNormChunk - 1) / block::kNormChunk;
+    int waves = 1;
+    while (waves * block::kQuantChunks < chunks)
+        waves *= 2;
+    while (waves < block::kQuantMaxWaves && waves < chunks && a->n_rows * waves < 8192)
+        waves *= 2;
+    qa.row_waves = waves;
+    qa.chunks = (chunks + waves - 1) / waves;
+    // a launch's work-items must fit in 32 bits
+    if (a->n_rows > ((int64_t)UINT32_MAX - 1024) / (waves * ep::kWave))
+        return fail(EP_ERR_SIZE, "args.n_rows = %lld is too large for one launch",
+                    (long long)a->n_rows);
+    const hipError_t e =
+        block::launch_quantize(qa, a->dtype == EP_BF16 ? 0 : 1,
+                               a->n_rows * a->hidden * 3 > kKeepBytes,
+                               static_cast<hipStream_t>(stream_ptr));
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "quantize_int8 launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int moe_grouped_gemm_int8(const moe_grouped_gemm_int8_args_t* a, void* stream_ptr)
+{
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    const bool swiglu = a->epilogue == MOE_EPILOGUE_SWIGLU;
+    if (!swiglu && a->epilogue != MOE_EPILOGUE_ROWS)
+        return fail(EP_ERR_ARG, "args.epilogue = %d: must be a MOE_EPILOGUE_* value", a->epilogue);
+    if (a->out_dtype != EP_BF16 && a->out_dtype != EP_FP16)
+        return fail(EP_ERR_ARG, "args.out_dtype = %d: must be EP_BF16 or EP_FP16", a->out_dtype);
+    if (a->groups < 0 || a->cap < 0)
+        return fail(EP_ERR_ARG, "args.groups = %d, args.cap = %d: must be >= 0", a->groups, a->cap);
+    if (a->k < 16 || a->k % 16)
+        return fail(EP_ERR_ARG, "args.k = %d: must be a positive multiple of 16", a->k);
+    const int step = swiglu ? 16 : 8;
+    if (a->n < step || a->n % step)
+        return fail(EP_ERR_ARG, "args.n = %d: must be a positive multiple of %d", a->n, step);
+    if (a->n > (1 << 20) || a->k > (1 << 16) || a->groups > (1 << 20))
+        return fail(EP_ERR_SIZE, "args.n = %d, args.k = %d, args.groups = %d: must be at most "
+                    "2^20, 2^16 and 2^20", a->n, a->k, a->groups);
+    if ((int64_t)a->groups * a->cap > INT32_MAX)
+        return fail(EP_ERR_SIZE, "args.groups * args.cap = %lld exceeds 2^31 - 1",
+                    (long long)a->groups * a->cap);
+    if (a->groups == 0 || a->cap == 0)
+        return ok();
+    const Pointer ptrs[] = {{a->a, "args.a", kPtrAlign, true},
+                            {a->a_scales, "args.a_scales", 4, true},
+                            {a->b, "args.b", kPtrAlign, true},
+                            {a->b_scales, "args.b_scales", 4, true},
+                            {a->counts, "args.counts", 4, false},
+                            {a->out, "args.out", kPtrAlign, true}};
+    const int rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+    block::GemmArgs ga;
+    ga.a = static_cast<const uint8_t*>(a->a);
+    ga.as = a->a_scales;
+    ga.b = static_cast<const uint8_t*>(a->b);
+    ga.bs = a->b_scales;
+    ga.counts = a->counts;
+    ga.out = static_cast<uint8_t*>(a->out);
+    ga.groups = a->groups;
+    ga.cap = a->cap;
+    ga.n = a->n;
+    ga.k = a->k;
+    ga.col_tiles = (a->n + 255) / 256;
+    const hipError_t e = block::launch_gemm(ga, a->out_dtype == EP_FP16 ? 1 : 0, swiglu,
+                                            kGemmBlocks, static_cast<hipStream_t>(stream_ptr));
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "grouped_gemm_int8 launch failed: %s", hipGetErrorString(e));
     return ok();
 }
 

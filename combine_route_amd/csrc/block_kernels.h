@@ -75,4 +75,37 @@ struct NormBackwardArgs {
 hipError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int wtype, bool stream,
                                 hipStream_t s);
 
+// block_quantize.hip: rows to INT8 rows. A wave keeps up to kQuantChunks
+// chunks of its row in registers.
+constexpr int kQuantChunks = 8;
+constexpr int kQuantMaxWaves = 16;
+constexpr int kQuantMaxHidden = kNormChunk * kQuantChunks * kQuantMaxWaves;
+
+struct QuantizeArgs {
+    const uint8_t* rows;
+    uint8_t* codes;
+    float* scales;
+    const int32_t* counts;       // or null
+    int64_t n_rows, group_rows;
+    int32_t H;
+    int32_t row_waves;           // waves a row: a power of two up to kQuantMaxWaves
+    int32_t chunks;              // chunks a wave, <= kQuantChunks
+};
+
+hipError_t launch_quantize(const QuantizeArgs& a, int dtype, bool stream, hipStream_t s);
+
+// block_gemm.hip: the grouped INT8 product.
+struct GemmArgs {
+    const uint8_t* a;            // [groups][cap][k] int8
+    const float* as;             // [groups][cap]
+    const uint8_t* b;            // [groups][n][k] int8
+    const float* bs;             // [groups][n]
+    const int32_t* counts;       // [groups] or null
+    uint8_t* out;                // [groups][cap][n or n / 2] bf16 / fp16
+    int32_t groups, cap, n, k;
+    int32_t col_tiles;           // of 256 weight rows: ceil(n / 256), ceil(n / 2 / 128) of swiglu
+};
+
+hipError_t launch_gemm(const GemmArgs& a, int dtype, bool swiglu, int blocks, hipStream_t s);
+
 }  // namespace block

@@ -151,6 +151,75 @@ size_t moe_block_norm_backward_workspace_bytes(int64_t rows, int32_t hidden, int
 
 int moe_block_norm_backward(const moe_block_norm_backward_args_t *args, void *stream);
 
+/* Rows of bf16 / fp16 quantized to INT8 rows with a scale per row (above).
+ *   rows          [n_rows][hidden] of dtype (EP_BF16 or EP_FP16).
+ *   codes, scales [n_rows][hidden] int8, [n_rows] float.
+ *   row_counts, group_rows  as moe_rms_norm: only the first row_counts[g] rows
+ *                 of group g are read and written.
+ * hidden: a multiple of 8, 8 to 65536; rows and codes 16-byte aligned, scales
+ * and row_counts 4-byte. Errors: EP_ERR_NULL, EP_ERR_ALIGN, EP_ERR_ARG,
+ * EP_ERR_SIZE, EP_ERR_HIP. n_rows == 0 returns EP_OK whatever the pointers
+ * are. */
+typedef struct moe_quantize_int8_args {
+    const void *rows;
+    void *codes;
+    float *scales;
+    const int32_t *row_counts;
+    int64_t n_rows;
+    int64_t group_rows;
+    int32_t hidden;
+    int32_t dtype;
+} moe_quantize_int8_args_t;
+
+int moe_quantize_int8(const moe_quantize_int8_args_t *args, void *stream);
+
+/* Grouped product of expert-major INT8 rows with the experts' INT8 weights, a
+ * scale per row (token) on one side and per weight row (output channel) on
+ * the other: for group g (an expert), row i < min(counts[g], cap) and weight
+ * row j,
+ *   y[g][i][j] = a_scales[g][i] * (b_scales[g][j] * sum over e of
+ *                a[g][i][e] * b[g][j][e])
+ * The sum is exact, in 32-bit integers; its conversion to FP32 and the product
+ * with b_scales round once each.
+ *   MOE_EPILOGUE_ROWS rounds the product with a_scales to FP32 and then to
+ * bf16, or at once to fp16. MOE_EPILOGUE_SWIGLU takes weight rows [0, n / 2) as
+ * the gate and [n / 2, n) as the up projection, both in FP32, and rounds z =
+ * gate / (1 + exp(-gate)) * up (FP32) to out_dtype: the rows that
+ * moe_quantize_int8 makes the next product's input of.
+ *   a, a_scales   [groups][cap][k] int8, [groups][cap] float: the packed rows
+ *                 and scales of a dispatch of INT8 rows (dispatch_dtype
+ *                 EP_FP8_E4M3, whose payload it moves as bytes, with one
+ *                 4-byte scale a row), or moe_quantize_int8's.
+ *   b, b_scales   [groups][n][k] int8, [groups][n] float.
+ *   counts        device int32 [groups] (packed_count; a count above cap means
+ *                 cap, one below 0 none), or NULL: cap rows each.
+ *   out           ROWS: [groups][cap][n] of out_dtype (EP_BF16 or EP_FP16).
+ *                 SWIGLU: [groups][cap][n / 2].
+ * Codes of -128 are as any other. Rows past a group's count are neither read
+ * nor written. k: a positive multiple of 16 up to 65536 (the sum stays below
+ * 2^31); n: a positive multiple of 8 (ROWS) or 16 (SWIGLU); n and groups at
+ * most 2^20, groups, cap >= 0. A row's result depends on its own inputs
+ * alone. a, b and out 16-byte aligned, the rest 4-byte.
+ * Errors: EP_ERR_NULL, EP_ERR_ALIGN, EP_ERR_ARG, EP_ERR_SIZE (n, k or groups
+ * too large, or groups * cap above 2^31 - 1), EP_ERR_HIP. groups == 0 or cap
+ * == 0 returns EP_OK whatever the pointers are. */
+typedef struct moe_grouped_gemm_int8_args {
+    const void *a;
+    const float *a_scales;
+    const void *b;
+    const float *b_scales;
+    const int32_t *counts;
+    void *out;
+    int32_t groups;
+    int32_t cap;
+    int32_t n;
+    int32_t k;
+    int32_t out_dtype;
+    int32_t epilogue;
+} moe_grouped_gemm_int8_args_t;
+
+int moe_grouped_gemm_int8(const moe_grouped_gemm_int8_args_t *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -115,13 +115,76 @@ def test_block_norm_backward_refuses(fn, change, code, word):
     assert word in cra.ep_last_error()
 
 
+QUANT = dict(rows=FAKE, codes=FAKE, scales=FAKE, row_counts=FAKE, n_rows=64, group_rows=16,
+             hidden=256, dtype=cra.EP_BF16)
+
+
+@pytest.mark.parametrize("change,code,word", [
+    (dict(rows=None), cra.EP_ERR_NULL, "rows"),
+    (dict(codes=None), cra.EP_ERR_NULL, "codes"),
+    (dict(scales=None), cra.EP_ERR_NULL, "scales"),
+    (dict(rows=FAKE + 8), cra.EP_ERR_ALIGN, "rows"),
+    (dict(codes=FAKE + 8), cra.EP_ERR_ALIGN, "codes"),
+    (dict(scales=FAKE + 2), cra.EP_ERR_ALIGN, "scales"),
+    (dict(row_counts=FAKE + 1), cra.EP_ERR_ALIGN, "row_counts"),
+    (dict(n_rows=-1), cra.EP_ERR_ARG, "n_rows"),
+    (dict(group_rows=0), cra.EP_ERR_ARG, "group_rows"),
+    (dict(group_rows=7), cra.EP_ERR_ARG, "group_rows"),
+    (dict(hidden=0), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=12), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=65536 + 8), cra.EP_ERR_SIZE, "hidden"),
+    (dict(dtype=block.MOE_INT8), cra.EP_ERR_ARG, "dtype"),
+    (dict(n_rows=1 << 27, group_rows=1 << 20), cra.EP_ERR_SIZE, "n_rows"),
+])
+def test_quantize_int8_refuses(fn, change, code, word):
+    a = block.MoeQuantizeInt8Args(**dict(QUANT, **change))
+    assert fn("moe_quantize_int8")(ctypes.byref(a), None) == code
+    assert word in cra.ep_last_error()
+
+
+GEMM = dict(a=FAKE, a_scales=FAKE, b=FAKE, b_scales=FAKE, counts=FAKE, out=FAKE, groups=4, cap=16,
+            n=256, k=128, out_dtype=cra.EP_BF16, epilogue=cra.MOE_EPILOGUE_ROWS)
+
+
+@pytest.mark.parametrize("change,code,word", [
+    (dict(epilogue=2), cra.EP_ERR_ARG, "epilogue"),
+    (dict(out_dtype=cra.EP_FP8_E4M3), cra.EP_ERR_ARG, "out_dtype"),
+    (dict(out_dtype=block.MOE_INT8, epilogue=cra.MOE_EPILOGUE_SWIGLU), cra.EP_ERR_ARG,
+     "out_dtype"),
+    (dict(groups=-1), cra.EP_ERR_ARG, "groups"),
+    (dict(cap=-1), cra.EP_ERR_ARG, "cap"),
+    (dict(k=0), cra.EP_ERR_ARG, "args.k"),
+    (dict(k=24), cra.EP_ERR_ARG, "args.k"),
+    (dict(k=65536 + 16), cra.EP_ERR_SIZE, "args.k"),
+    (dict(n=0), cra.EP_ERR_ARG, "args.n"),
+    (dict(n=12), cra.EP_ERR_ARG, "args.n"),
+    (dict(n=24, epilogue=cra.MOE_EPILOGUE_SWIGLU), cra.EP_ERR_ARG, "args.n"),
+    (dict(n=(1 << 20) + 16), cra.EP_ERR_SIZE, "args.n"),
+    (dict(groups=(1 << 20) + 1), cra.EP_ERR_SIZE, "groups"),
+    (dict(groups=1 << 20, cap=1 << 11), cra.EP_ERR_SIZE, "cap"),
+] + [(dict({p: None}), cra.EP_ERR_NULL, p) for p in ("a", "a_scales", "b", "b_scales", "out")] +
+    [(dict({p: FAKE + 8}), cra.EP_ERR_ALIGN, p) for p in ("a", "b", "out")] +
+    [(dict({p: FAKE + 2}), cra.EP_ERR_ALIGN, p) for p in ("a_scales", "b_scales", "counts")])
+def test_grouped_gemm_int8_refuses(fn, change, code, word):
+    a = block.MoeGroupedGemmInt8Args(**dict(GEMM, **change))
+    assert fn("moe_grouped_gemm_int8")(ctypes.byref(a), None) == code
+    assert word in cra.ep_last_error()
+
+
 def test_calls_without_rows_are_no_work(fn):
     a = block.MoeBlockNormArgs(**dict(NORM, rows=0, y=None, residual=None))
     assert fn("moe_block_norm")(ctypes.byref(a), None) == cra.EP_OK
     a = block.MoeBlockNormBackwardArgs(**dict(BACKWARD, rows=0, y=None, workspace=None))
     assert fn("moe_block_norm_backward")(ctypes.byref(a), None) == cra.EP_OK
+    a = block.MoeQuantizeInt8Args(**dict(QUANT, n_rows=0, rows=None))
+    assert fn("moe_quantize_int8")(ctypes.byref(a), None) == cra.EP_OK
+    for change in (dict(groups=0, a=None), dict(cap=0, out=None)):
+        a = block.MoeGroupedGemmInt8Args(**dict(GEMM, **change))
+        assert fn("moe_grouped_gemm_int8")(ctypes.byref(a), None) == cra.EP_OK
     assert cra.ep_last_error() == ""
-    for name in ("moe_block_norm", "moe_block_norm_backward"):
+    for name in block.BLOCK_EXPORTED:
+        if name.endswith("_bytes"):
+            continue
         assert fn(name)(None, None) == cra.EP_ERR_NULL
 
 
@@ -147,6 +210,13 @@ def test_tensors_off_the_gpu_are_refused():
         cra.moe_block_norm([1.0], x, w, 1e-6)
     with pytest.raises(ValueError, match="GPU"):
         cra.moe_block_norm_backward(x, x, 1e-6, x, grad_out=x, pre_weight=w)
+    with pytest.raises(ValueError, match="GPU"):
+        cra.moe_quantize_int8(x, x, w)
+    for call in (cra.moe_grouped_gemm_int8, cra.moe_grouped_gemm_int8_swiglu):
+        with pytest.raises(ValueError, match="GPU"):
+            call(x, w, x, w, x)
+        with pytest.raises(TypeError, match="a must"):
+            call([1], w, x, w, x)
 
 
 def test_the_other_headers_are_as_they_were():
