@@ -1026,4 +1026,5 @@ from .moe import (MOE_EPILOGUE_ROWS, MOE_EPILOGUE_SWIGLU, MOE_EXPORTED,  # noqa:
                   moe_grouped_gemm_swiglu, moe_rms_norm)
 from .block import (BLOCK_EXPORTED, MOE_INT8, moe_block_norm,  # noqa: E402
                     moe_block_norm_backward, moe_block_norm_backward_workspace_bytes,
-                    moe_grouped_gemm_int8, moe_grouped_gemm_int8_swiglu, moe_quantize_int8)
+                    moe_few_tokens, moe_few_tokens_workspace_bytes, moe_grouped_gemm_int8,
+                    moe_grouped_gemm_int8_swiglu, moe_quantize_int8)

@@ -16,7 +16,7 @@ from .moe import (_CODES, _DTYPE_CODE, _ROWS, MOE_EPILOGUE_ROWS, MOE_EPILOGUE_SW
 MOE_INT8 = 4
 BLOCK_EXPORTED = ("moe_block_norm", "moe_block_norm_backward",
                   "moe_block_norm_backward_workspace_bytes", "moe_quantize_int8",
-                  "moe_grouped_gemm_int8")
+                  "moe_grouped_gemm_int8", "moe_few_tokens", "moe_few_tokens_workspace_bytes")
 
 _INT8 = (torch.int8,)
 
@@ -53,6 +53,14 @@ class MoeGroupedGemmInt8Args(ctypes.Structure):
                                                "epilogue")])
 
 
+class MoeFewTokensArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "x", "indices", "weights", "gate_up", "gate_up_scales", "down", "down_scales", "out",
+        "workspace")] + [("workspace_bytes", ctypes.c_int64)] +
+        [(n, ctypes.c_int32) for n in ("tokens", "topk", "experts", "hidden", "inter", "dtype",
+                                       "weight_dtype")])
+
+
 def _declare(lib):
     """The functions of include/moe_block.h by name, with their types."""
     V, P = ctypes.c_void_p, ctypes.POINTER
@@ -62,6 +70,8 @@ def _declare(lib):
                                                             ctypes.c_int64]
     lib.moe_quantize_int8.argtypes = [P(MoeQuantizeInt8Args), V]
     lib.moe_grouped_gemm_int8.argtypes = [P(MoeGroupedGemmInt8Args), V]
+    lib.moe_few_tokens.argtypes = [P(MoeFewTokensArgs), V]
+    lib.moe_few_tokens_workspace_bytes.argtypes = [ctypes.c_int32] * 4
     fns = {name: getattr(lib, name) for name in BLOCK_EXPORTED}
     for name, fn in fns.items():
         fn.restype = ctypes.c_size_t if name.endswith("_bytes") else ctypes.c_int
@@ -309,3 +319,53 @@ def moe_grouped_gemm_int8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, b: tor
     gets silu(gate) * up, which moe_quantize_int8 makes the next product's rows
     of."""
     _product(a, a_scales, b, b_scales, out, counts, stream, MOE_EPILOGUE_SWIGLU)
+
+
+def moe_few_tokens_workspace_bytes(tokens: int, topk: int, hidden: int, inter: int) -> int:
+    """Bytes of workspace that moe_few_tokens needs."""
+    return _workspace_bytes("moe_few_tokens_workspace_bytes", tokens, topk, hidden, inter)
+
+
+def moe_few_tokens(x: torch.Tensor, indices: torch.Tensor, weights: Optional[torch.Tensor],
+                   gate_up: torch.Tensor, gate_up_scales: torch.Tensor, down: torch.Tensor,
+                   down_scales: torch.Tensor, out: torch.Tensor,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_few_tokens() (include/moe_block.h): the experts of a whole layer for up
+    to 64 tokens, without a dispatch. x [..., H] (bf16 or fp16) and out of its
+    shape and type; indices and weights (or None: 1 each) [..., k] of the same
+    leading sizes; gate_up [E, 2 I, H] and down [E, H, I] as expert_mlp's (E4M3,
+    scales [E, 2 I / 128, H / 128] and [E, H / 128, I / 128]) or expert_mlp_int8's
+    (int8, scales [E, 2 I] and [E, H]). workspace: any tensor of
+    moe_few_tokens_workspace_bytes bytes that no other call uses at the same
+    time; None makes a new one."""
+    index, shape, H, tokens, dtype = _rows_of(x, "x")
+    for t, name in ((indices, "indices"), (gate_up, "gate_up"), (down, "down"),
+                    (gate_up_scales, "gate_up_scales"), (down_scales, "down_scales"),
+                    (out, "out")):
+        _index_of(t, name)
+    for t, name in ((gate_up, "gate_up"), (down, "down")):
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have 3 dimensions, not {t.dim()}")
+    if indices.dim() == 0:
+        raise ValueError("indices must have slots")
+    topk = indices.shape[-1]
+    E, inter = down.shape[0], down.shape[2]
+    int8 = gate_up.dtype == torch.int8
+    codes = _INT8 if int8 else _CODES
+    scales = (((E, 2 * inter), (E, H)) if int8 else
+              ((E, 2 * inter // 128, H // 128), (E, H // 128, inter // 128)))
+    slots = shape[:-1] + (topk,)
+    ws, nbytes = None, 0
+    if tokens:
+        nbytes = moe_few_tokens_workspace_bytes(tokens, topk, H, inter)
+        ws = _workspace(workspace, nbytes, index, stream)
+    a = MoeFewTokensArgs(
+        _ptr(x, "x", shape, (x.dtype,), index), _ptr(indices, "indices", slots, _I32, index),
+        _ptr(weights, "weights", slots, _F32, index),
+        _ptr(gate_up, "gate_up", (E, 2 * inter, H), codes, index),
+        _ptr(gate_up_scales, "gate_up_scales", scales[0], _F32, index),
+        _ptr(down, "down", (E, H, inter), codes, index),
+        _ptr(down_scales, "down_scales", scales[1], _F32, index),
+        _ptr(out, "out", shape, (x.dtype,), index), None if ws is None else ws.data_ptr(), nbytes,
+        tokens, topk, E, H, inter, dtype, MOE_INT8 if int8 else EP_FP8_E4M3)
+    _call("moe_few_tokens", index, stream, a)

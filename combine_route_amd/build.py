@@ -14,7 +14,8 @@ SOURCES = [os.path.join(PKG, "csrc", f)
            for f in ("ep_plan.cpp", "ep_kernels.hip", "ep_expert.hip", "ep_wire.hip",
                      "ep_standard.hip", "ep_probe.hip", "ep_static.hip", "moe_host.cpp",
                      "moe_norm.hip", "moe_backward.hip", "moe_gemm.hip", "block_host.cpp",
-                     "block_norm.hip", "block_backward.hip", "block_quantize.hip", "block_gemm.hip")]
+                     "block_norm.hip", "block_backward.hip", "block_quantize.hip", "block_gemm.hip",
+                     "block_few.hip")]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -127,6 +127,17 @@ bool backward_shape(int64_t rows, int hidden, int64_t groups, BackwardShape* s)
     return true;
 }
 
+// Bytes of moe_few_tokens's workspace, 0 for sizes it refuses: the hidden rows
+// of every slot, as bf16 values and their rests.
+size_t few_bytes(int tokens, int topk, int hidden, int inter)
+{
+    if (tokens < 1 || tokens > block::kFewMaxTokens || topk < 1 || topk > 64 ||
+        tokens * topk > block::kFewMaxSlots || hidden < 16 || hidden > 65536 || hidden % 16 ||
+        inter < 16 || inter > 65536 || inter % 16)
+        return 0;
+    return (size_t)4 * tokens * topk * inter;
+}
+
 }  // namespace
 
 extern "C" {
@@ -410,6 +421,94 @@ int moe_grouped_gemm_int8(const moe_grouped_gemm_int8_args_t* a, void* stream_pt
                                             kGemmBlocks, static_cast<hipStream_t>(stream_ptr));
     if (e != hipSuccess)
         return fail(EP_ERR_HIP, "grouped_gemm_int8 launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+size_t moe_few_tokens_workspace_bytes(int32_t tokens, int32_t topk, int32_t hidden, int32_t inter)
+{
+    const size_t n = few_bytes(tokens, topk, hidden, inter);
+    if (n == 0)
+        fail(EP_ERR_ARG,
+             "tokens = %d, topk = %d, hidden = %d, inter = %d: must be 1 to %d, 1 to 64 (at most "
+             "%d slots) and multiples of 16 up to 65536",
+             tokens, topk, hidden, inter, block::kFewMaxTokens, block::kFewMaxSlots);
+    else
+        ok();
+    return n;
+}
+
+int moe_few_tokens(const moe_few_tokens_args_t* a, void* stream_ptr)
+{
+    if (!a)
+        return fail(EP_ERR_NULL, "args is NULL");
+    if (a->dtype != EP_BF16 && a->dtype != EP_FP16)
+        return fail(EP_ERR_ARG, "args.dtype = %d: must be EP_BF16 or EP_FP16", a->dtype);
+    if (a->weight_dtype != EP_FP8_E4M3 && a->weight_dtype != MOE_INT8)
+        return fail(EP_ERR_ARG, "args.weight_dtype = %d: must be EP_FP8_E4M3 or MOE_INT8",
+                    a->weight_dtype);
+    const int step = a->weight_dtype == MOE_INT8 ? 16 : 128;
+    if (a->hidden < step || a->hidden % step)
+        return fail(EP_ERR_ARG, "args.hidden = %d: must be a positive multiple of %d", a->hidden,
+                    step);
+    if (a->inter < step || a->inter % step)
+        return fail(EP_ERR_ARG, "args.inter = %d: must be a positive multiple of %d", a->inter,
+                    step);
+    if (a->tokens < 0 || a->topk < 1 || a->experts < 1)
+        return fail(EP_ERR_ARG,
+                    "args.tokens = %d, args.topk = %d, args.experts = %d: must be >= 0, 1 and 1",
+                    a->tokens, a->topk, a->experts);
+    if (a->tokens > block::kFewMaxTokens || a->topk > 64 ||
+        a->tokens * a->topk > block::kFewMaxSlots || a->experts > block::kFewMaxExperts ||
+        a->hidden > 65536 || a->inter > 65536)
+        return fail(EP_ERR_SIZE,
+                    "args.tokens = %d, args.topk = %d, args.experts = %d, args.hidden = %d, "
+                    "args.inter = %d: must be at most %d, 64 (%d slots in all), %d, 65536 and "
+                    "65536",
+                    a->tokens, a->topk, a->experts, a->hidden, a->inter, block::kFewMaxTokens,
+                    block::kFewMaxSlots, block::kFewMaxExperts);
+    if (a->tokens == 0)
+        return ok();
+    const Pointer ptrs[] = {{a->x, "args.x", kPtrAlign, true},
+                            {a->indices, "args.indices", 4, true},
+                            {a->weights, "args.weights", 4, false},
+                            {a->gate_up, "args.gate_up", kPtrAlign, true},
+                            {a->gate_up_scales, "args.gate_up_scales", 4, true},
+                            {a->down, "args.down", kPtrAlign, true},
+                            {a->down_scales, "args.down_scales", 4, true},
+                            {a->out, "args.out", kPtrAlign, true},
+                            {a->workspace, "args.workspace", kPtrAlign, true}};
+    const int rc = check_pointers(ptrs);
+    if (rc != EP_OK)
+        return rc;
+    const int64_t need = (int64_t)few_bytes(a->tokens, a->topk, a->hidden, a->inter);
+    if (a->workspace_bytes < need)
+        return fail(EP_ERR_SIZE, "args.workspace_bytes = %lld: %lld are needed",
+                    (long long)a->workspace_bytes, (long long)need);
+    block::FewArgs fa;
+    fa.x = static_cast<const uint8_t*>(a->x);
+    fa.ids = a->indices;
+    fa.w = a->weights;
+    fa.up = static_cast<const uint8_t*>(a->gate_up);
+    fa.ups = a->gate_up_scales;
+    fa.down = static_cast<const uint8_t*>(a->down);
+    fa.downs = a->down_scales;
+    fa.out = static_cast<uint8_t*>(a->out);
+    fa.act = static_cast<uint8_t*>(a->workspace);
+    fa.T = a->tokens;
+    fa.topk = a->topk;
+    fa.E = a->experts;
+    fa.H = a->hidden;
+    fa.I = a->inter;
+    fa.hits = std::min(a->experts, a->tokens * a->topk);
+    // Pieces of inter in the down product, so that a single token's experts
+    // occupy a block's waves; by topk alone, so that a token's sums are the
+    // same in every call.
+    fa.splits = a->topk >= 8 ? 1 : a->topk >= 4 ? 2 : 4;
+    const hipError_t e = block::launch_few(fa, a->dtype == EP_BF16 ? 0 : 1,
+                                           a->weight_dtype == MOE_INT8 ? 1 : 0,
+                                           static_cast<hipStream_t>(stream_ptr));
+    if (e != hipSuccess)
+        return fail(EP_ERR_HIP, "few_tokens launch failed: %s", hipGetErrorString(e));
     return ok();
 }
 

@@ -108,4 +108,27 @@ struct GemmArgs {
 
 hipError_t launch_gemm(const GemmArgs& a, int dtype, bool swiglu, int blocks, hipStream_t s);
 
+// block_few.hip: a layer's experts for a few tokens.
+constexpr int kFewMaxTokens = 64;
+constexpr int kFewMaxSlots = 1024;   // tokens * topk
+constexpr int kFewMaxExperts = 65536;
+
+struct FewArgs {
+    const uint8_t* x;            // [T][H] bf16 / fp16
+    const int32_t* ids;          // [T][topk]
+    const float* w;              // [T][topk] or null
+    const uint8_t* up;           // [E][2 I][H] E4M3 or int8
+    const float* ups;
+    const uint8_t* down;         // [E][H][I]
+    const float* downs;
+    uint8_t* out;                // [T][H]
+    uint8_t* act;                // [2][T * topk][I] bf16: hidden values, their rests
+    int32_t T, topk, E, H, I;
+    int32_t hits;                // most experts a call of these sizes can hit
+    int32_t splits;              // pieces of I in the down product
+};
+
+// dtype: 0 bf16, 1 fp16; wtype: 0 E4M3, 1 int8.
+hipError_t launch_few(const FewArgs& a, int dtype, int wtype, hipStream_t s);
+
 }  // namespace block

@@ -220,6 +220,64 @@ typedef struct moe_grouped_gemm_int8_args {
 
 int moe_grouped_gemm_int8(const moe_grouped_gemm_int8_args_t *args, void *stream);
 
+/* A whole layer's experts for a few tokens, in two kernels and without a
+ * dispatch: for each token t, over the distinct experts e that its slots name
+ * (ids outside 0 .. experts - 1 name none), in the order of their first slots,
+ *   out[t] = sum of c * down_e (silu(gate_e x_t) * (up_e x_t))
+ * c: the FP32 sum in slot order of the weights of the token's slots that name
+ * e, 1 without weights; as combine_standard_moe with every expert on hand and
+ * no capacity. It reads the weights of the experts that are hit, once each in
+ * calls of up to 16 tokens an expert, and nothing else of their size.
+ *   x             [tokens][hidden] of dtype (EP_BF16 or EP_FP16), taken as it
+ *                 is: neither x nor the hidden rows are quantized.
+ *   indices       [tokens][topk] int32.
+ *   weights       [tokens][topk] float, or NULL.
+ *   gate_up       [experts][2 * inter][hidden] of weight_dtype, gate rows then
+ *                 up rows; down [experts][hidden][inter].
+ *   gate_up_scales, down_scales  as expert_mlp's or expert_mlp_int8's:
+ *                 EP_FP8_E4M3: float per 128 x 128 block, [experts][2 * inter
+ *                 / 128][hidden / 128] and [experts][hidden / 128][inter /
+ *                 128]; MOE_INT8: float per weight row, [experts][2 * inter]
+ *                 and [experts][hidden].
+ *   out           [tokens][hidden] of dtype; 0 for a token without experts.
+ *   workspace     moe_few_tokens_workspace_bytes(tokens, topk, hidden, inter)
+ *                 bytes, 16-byte aligned, overwritten.
+ * Products of x and of the hidden rows (as a bf16 value and the bf16 value of
+ * its rest, 16 bits) with the weights' codes, both exact in the matrix units'
+ * operands, are summed in FP32; scales, silu, c and the sum over experts are
+ * FP32 and out is rounded once. A token's result does not depend on the other
+ * tokens of the call.
+ * tokens 0 to 64, topk 1 to 64, tokens * topk at most 1024; hidden and inter
+ * multiples of 128 (EP_FP8_E4M3) or 16 (MOE_INT8) up to 65536; experts 1 to
+ * 65536. x, gate_up, down and out 16-byte aligned, the rest 4-byte.
+ * Errors: EP_ERR_NULL, EP_ERR_ALIGN, EP_ERR_ARG, EP_ERR_SIZE (a size or
+ * workspace_bytes), EP_ERR_HIP. tokens == 0 returns EP_OK whatever the
+ * pointers are. */
+typedef struct moe_few_tokens_args {
+    const void *x;
+    const int32_t *indices;
+    const float *weights;
+    const void *gate_up;
+    const float *gate_up_scales;
+    const void *down;
+    const float *down_scales;
+    void *out;
+    void *workspace;
+    int64_t workspace_bytes;
+    int32_t tokens;
+    int32_t topk;
+    int32_t experts;
+    int32_t hidden;
+    int32_t inter;
+    int32_t dtype;
+    int32_t weight_dtype;
+} moe_few_tokens_args_t;
+
+/* 0 for sizes that the call refuses. */
+size_t moe_few_tokens_workspace_bytes(int32_t tokens, int32_t topk, int32_t hidden, int32_t inter);
+
+int moe_few_tokens(const moe_few_tokens_args_t *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

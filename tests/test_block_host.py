@@ -171,6 +171,51 @@ def test_grouped_gemm_int8_refuses(fn, change, code, word):
     assert word in cra.ep_last_error()
 
 
+FEW = dict(x=FAKE, indices=FAKE, weights=FAKE, gate_up=FAKE, gate_up_scales=FAKE, down=FAKE,
+           down_scales=FAKE, out=FAKE, workspace=FAKE, workspace_bytes=1 << 40, tokens=4, topk=2,
+           experts=8, hidden=256, inter=128, dtype=cra.EP_BF16, weight_dtype=cra.EP_FP8_E4M3)
+
+
+@pytest.mark.parametrize("change,code,word", [
+    (dict(dtype=cra.EP_FP8_E4M3), cra.EP_ERR_ARG, "args.dtype"),
+    (dict(weight_dtype=cra.EP_BF16), cra.EP_ERR_ARG, "weight_dtype"),
+    (dict(hidden=0), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=192), cra.EP_ERR_ARG, "hidden"),
+    (dict(hidden=200, weight_dtype=block.MOE_INT8), cra.EP_ERR_ARG, "hidden"),
+    (dict(inter=64), cra.EP_ERR_ARG, "inter"),
+    (dict(inter=8, weight_dtype=block.MOE_INT8), cra.EP_ERR_ARG, "inter"),
+    (dict(tokens=-1), cra.EP_ERR_ARG, "tokens"),
+    (dict(topk=0), cra.EP_ERR_ARG, "topk"),
+    (dict(experts=0), cra.EP_ERR_ARG, "experts"),
+    (dict(tokens=65), cra.EP_ERR_SIZE, "tokens"),
+    (dict(topk=65), cra.EP_ERR_SIZE, "topk"),
+    (dict(tokens=64, topk=17), cra.EP_ERR_SIZE, "slots"),
+    (dict(experts=65537), cra.EP_ERR_SIZE, "experts"),
+    (dict(hidden=65536 + 128), cra.EP_ERR_SIZE, "hidden"),
+    (dict(inter=65536 + 128), cra.EP_ERR_SIZE, "inter"),
+    (dict(workspace_bytes=4 * 4 * 2 * 128 - 1), cra.EP_ERR_SIZE, "workspace_bytes"),
+] + [(dict({p: None}), cra.EP_ERR_NULL, p) for p in (
+    "x", "indices", "gate_up", "gate_up_scales", "down", "down_scales", "out", "workspace")] +
+    [(dict({p: FAKE + 8}), cra.EP_ERR_ALIGN, p) for p in ("x", "gate_up", "down", "out",
+                                                         "workspace")] +
+    [(dict({p: FAKE + 2}), cra.EP_ERR_ALIGN, p) for p in ("indices", "weights", "gate_up_scales",
+                                                         "down_scales")])
+def test_few_tokens_refuses(fn, change, code, word):
+    a = block.MoeFewTokensArgs(**dict(FEW, **change))
+    assert fn("moe_few_tokens")(ctypes.byref(a), None) == code
+    assert word in cra.ep_last_error()
+
+
+def test_few_tokens_workspace_bytes(fn):
+    size = cra.moe_few_tokens_workspace_bytes
+    assert size(4, 2, 256, 128) == 4 * 8 * 128
+    assert size(64, 16, 16, 65536) == 4 * 1024 * 65536
+    for bad in ((0, 2, 256, 128), (65, 2, 256, 128), (64, 17, 256, 128), (4, 65, 256, 128),
+                (4, 2, 24, 128), (4, 2, 256, 8), (4, 2, 256, 65552)):
+        with pytest.raises(cra.EpError):
+            size(*bad)
+
+
 def test_calls_without_rows_are_no_work(fn):
     a = block.MoeBlockNormArgs(**dict(NORM, rows=0, y=None, residual=None))
     assert fn("moe_block_norm")(ctypes.byref(a), None) == cra.EP_OK
@@ -181,6 +226,8 @@ def test_calls_without_rows_are_no_work(fn):
     for change in (dict(groups=0, a=None), dict(cap=0, out=None)):
         a = block.MoeGroupedGemmInt8Args(**dict(GEMM, **change))
         assert fn("moe_grouped_gemm_int8")(ctypes.byref(a), None) == cra.EP_OK
+    a = block.MoeFewTokensArgs(**dict(FEW, tokens=0, x=None, workspace=None))
+    assert fn("moe_few_tokens")(ctypes.byref(a), None) == cra.EP_OK
     assert cra.ep_last_error() == ""
     for name in block.BLOCK_EXPORTED:
         if name.endswith("_bytes"):
@@ -217,6 +264,8 @@ def test_tensors_off_the_gpu_are_refused():
             call(x, w, x, w, x)
         with pytest.raises(TypeError, match="a must"):
             call([1], w, x, w, x)
+    with pytest.raises(ValueError, match="GPU"):
+        cra.moe_few_tokens(x, x, None, x, w, x, w, x)
 
 
 def test_the_other_headers_are_as_they_were():
