@@ -15,15 +15,15 @@
 // rows, each with up to 128 x 128 sums in registers: the fewest reads of LDS a
 // product (a wave of 128 x 64 would read 1.5 times as much, which with the
 // loads' writes is all that LDS can do while the matrix units are busy). For
-// each 64 elements of k (a step) the block holds both operands' slices in LDS,
+// each 64 or 128 elements of k (a step) the block holds both operands' slices in LDS,
 // loaded there directly from memory several steps before; a wave reads a
 // step's operands to registers during the step before, between the products.
 // One barrier a step: it says that the next step's slices are there and that
 // this step's, now in registers, may be overwritten.
 //
-// LDS slices are 64 bytes a row without padding; the four 16-byte chunks of a
-// row are permuted by a key of the row, so that any 8 rows a matrix operand
-// reads one after the other fall in different banks. The matrix instruction,
+// LDS slices are 64 or 128 bytes a row without padding; the 16-byte chunks of a
+// row are permuted by a key of the row, so that the rows a matrix operand reads
+// together fall in different banks. The matrix instruction,
 // v_mfma_i32_32x32x32_i8, has the weights as its rows and the token rows as
 // its columns; which weight row is which of its rows is chosen so that a lane
 // ends up with runs of 8 consecutive columns of one token row.
@@ -44,16 +44,17 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
 constexpr int kTileN = 256;   // weight rows a tile
-constexpr int kStep = 64;     // bytes of k a step
 constexpr int kSubs = 4;      // operands of 32 weight rows a wave
 constexpr int kMaxTS = 4;     // a tile of class TS has 64 TS rows
 constexpr int kTileRows = 64 * kMaxTS;
-constexpr int kBLoads = 4;    // 16-byte loads a lane and step, of weights
 
-constexpr int a_bytes(int ts) { return 64 * ts * kStep; }
-constexpr int stage_bytes(int ts) { return a_bytes(ts) + kTileN * kStep; }
+// Bytes of k a step: 128, whole cache lines of a row, where that leaves room for
+// three slices; else 64.
+constexpr int step_bytes(int ts) { return ts <= 2 ? 128 : 64; }
+constexpr int a_bytes(int ts) { return 64 * ts * step_bytes(ts); }
+constexpr int stage_bytes(int ts) { return a_bytes(ts) + kTileN * step_bytes(ts); }
 // Slices held: as many as fit.
-constexpr int stages(int ts) { return ts == 4 ? 4 : ts == 3 ? 5 : ts == 2 ? 6 : 7; }
+constexpr int stages(int ts) { return ts == 4 ? 4 : ts == 3 ? 5 : 3; }
 constexpr int kScaleBytes = (kTileRows + kTileN) * 4;
 constexpr int kScales = 144 * 1024;  // their place
 static_assert(stages(4) * stage_bytes(4) <= kScales && stages(3) * stage_bytes(3) <= kScales &&
@@ -69,22 +70,35 @@ struct Tile {
     int col;        // column tile
 };
 
-// The loads of a tile. Wave w's i-th 1 KB of a slice holds rows 16 * (4 * i +
-// w) .. + 15, a lane one 16-byte chunk of a row. Chunks past k are asked for
-// too, from beyond the resource's end (zeros, without memory traffic), so that
-// every step has the same loads in flight and no branch.
+// The loads of a tile. A wave's i-th 1 KB of a slice holds rows kRows * (4 * i +
+// wave) .. of kRows, a lane one 16-byte chunk of a row. Chunks past k are asked
+// for too, from beyond the resource's end (zeros, without memory traffic), so
+// that every step has the same loads in flight and no branch.
 // kSwiglu: weight rows [0, 128) of the tile are gate rows 128 * col .., rows
 // [128, 256) the up rows. Otherwise they are rows 256 * col .. .
 template <int TS, bool kSwiglu>
 struct Loads {
-    static constexpr int kAll = TS + kBLoads;  // a wave and step
+    static constexpr int kStep = step_bytes(TS);
+    static constexpr int kChunks = kStep / 16;          // of a row
+    static constexpr int kRows = kWave / kChunks;       // of a load
+    static constexpr int kALoads = 64 * TS / (4 * kRows);
+    static constexpr int kBLoads = kTileN / (4 * kRows);
+    static constexpr int kAll = kALoads + kBLoads;      // a wave and step
     u32x4 ra, rb0, rb1;                        // rows, the two halves of the weights
     u32x4 ras, rbs;                            // the rows' scales, this wave's weight rows'
-    uint32_t aoff, boff;
-    int aleft, bleft;                          // bytes of k from this lane's chunk on
-    uint32_t step64;                           // bytes of 64 rows of k
+    uint32_t off;                              // of this lane's chunk of the load's first rows
+    int left;                                  // bytes of k from this lane's chunk on
+    uint32_t rows4;                            // bytes of a load's rows of k, times 4
     uint32_t lds0;
     int wave;
+
+    // Place of a row's chunk: exclusive-or with it. The 16 rows that an operand
+    // reads together (lanes 0-3, 12-15, 20-27 of 32, and the others) lie in
+    // different banks so, of 64.
+    static __device__ __forceinline__ int key(int row)
+    {
+        return (row / (256 / kStep)) & (kChunks - 1);
+    }
 
     __device__ __forceinline__ Loads(const GemmArgs& a, const Tile& t, uint32_t block_lds0)
         : lds0(block_lds0)
@@ -92,14 +106,13 @@ struct Loads {
         const int lane = threadIdx.x & (kWave - 1);
         wave = uniform(threadIdx.x / kWave);
         const uint32_t K = (uint32_t)a.k;
-        const int lr = wave * 16 + (lane >> 2);  // row of i = 0; i adds 64
-        step64 = 64 * K;
-        const int achunk = (lane & 3) ^ ((lr >> 1) & 3);
-        const int bchunk = (lane & 3) ^ (((lr >> 1) & 1) | (((lr >> 3) & 1) << 1));
-        aoff = (uint32_t)lr * K + (uint32_t)achunk * 16u;
-        boff = (uint32_t)lr * K + (uint32_t)bchunk * 16u;
-        aleft = a.k - achunk * 16;
-        bleft = a.k - bchunk * 16;
+        const int lr = wave * kRows + lane / kChunks;  // row of i = 0; i adds 4 kRows
+        rows4 = 4 * kRows * K;
+        static_assert(4 * kRows * kStep % 256 == 0 && (4 * kRows * kStep / 256) % kChunks == 0,
+                      "the key of a load's rows does not depend on i");
+        const int chunk = (lane & (kChunks - 1)) ^ key(lr);
+        off = (uint32_t)lr * K + (uint32_t)chunk * 16u;
+        left = a.k - chunk * 16;
         ra = rsrc_words(a.a + t.row0 * K, t.rows * (int)K);
         const int64_t first = (int64_t)t.group * a.n;
         const int half = kSwiglu ? a.n / 2 : a.n;   // rows of one projection
@@ -114,28 +127,19 @@ struct Loads {
                        : rsrc_words(a.bs + first + r1, n1 * 4);
     }
 
-    __device__ __forceinline__ void row_load(int i, int h, int stage) const
-    {
-        const uint32_t past = h * kStep < aleft ? 0u : 1u << 30;
-        load_to_lds<false>(ra, lds0 + stage * stage_bytes(TS) + i * 4096 + wave * 1024,
-                           aoff + i * step64 + past, (uint32_t)h * kStep);
-    }
-
-    __device__ __forceinline__ void weight_load(int i, int h, int stage) const
-    {
-        const uint32_t past = h * kStep < bleft ? 0u : 1u << 30;
-        load_to_lds<(TS < kMaxTS)>(i < 2 ? rb0 : rb1,
-                    lds0 + stage * stage_bytes(TS) + a_bytes(TS) + i * 4096 + wave * 1024,
-                    boff + (i & 1) * step64 + past, (uint32_t)h * kStep);
-    }
-
-    // Load i of step h's.
+    // Load i of step h's, to its stage: the rows', then the weights'.
     __device__ __forceinline__ void load(int i, int h, int stage) const
     {
-        if (i < TS)
-            row_load(i, h, stage);
+        const uint32_t at = off + (h * kStep < left ? 0u : 1u << 30);
+        const uint32_t dst = lds0 + stage * stage_bytes(TS) + i * 4096 + wave * 1024;
+        constexpr int kHalf = kBLoads / 2;
+        if (i < kALoads)
+            load_to_lds<false>(ra, dst, at + i * rows4, (uint32_t)h * kStep);
+        else if (i < kALoads + kHalf)
+            load_to_lds<(TS < kMaxTS)>(rb0, dst, at + (i - kALoads) * rows4, (uint32_t)h * kStep);
         else
-            weight_load(i - TS, h, stage);
+            load_to_lds<(TS < kMaxTS)>(rb1, dst, at + (i - kALoads - kHalf) * rows4,
+                                       (uint32_t)h * kStep);
     }
 
     // The scales (to block `which` of them) and the first slices.
@@ -153,10 +157,11 @@ struct Loads {
     }
 };
 
-// A wave's operands of one step.
+// A wave's operands of one step: 32 bytes of k each.
 template <int TS>
 struct Operands {
-    i32x4 w[kSubs][2], t[TS][2];
+    static constexpr int kParts = step_bytes(TS) / 32;
+    i32x4 w[kSubs][kParts], t[TS][kParts];
 };
 
 // The sums of one tile, whose first slices are on their way.
@@ -165,33 +170,32 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
                                          i32x16 (&acc)[TS][kSubs])
 {
     using L = Loads<TS, kSwiglu>;
-    constexpr int S = stages(TS);
+    constexpr int S = stages(TS), kStep = L::kStep, kParts = Operands<TS>::kParts;
     const int lane = threadIdx.x & (kWave - 1);
     const int wm = ld.wave >> 1, wn = ld.wave & 1;
     const int q = lane >> 5, i32 = lane & 31;
     // the weight row that is row i32 of an operand: runs of 8 for a lane of
     // the result, which holds rows 8 b + 4 q + t, b and t 0 .. 3
     const int b = i32 >> 3, j = (b >> 1) * 16 + ((i32 >> 2) & 1) * 8 + (b & 1) * 4 + (i32 & 3);
-    const int wkey = ((j >> 1) & 1) | (((j >> 3) & 1) << 1);
     const int wrow = wn * (kSwiglu ? 64 : 128) + j;
-    const uint32_t wat = a_bytes(TS) + (uint32_t)wrow * kStep + (uint32_t)((q ^ wkey) * 16);
+    const uint32_t wat = a_bytes(TS) + (uint32_t)wrow * kStep + (uint32_t)((q ^ L::key(wrow)) * 16);
     const int trow = wm * 32 * TS + i32;
-    const uint32_t tat = (uint32_t)trow * kStep + (uint32_t)((q ^ ((trow >> 1) & 3)) * 16);
+    const uint32_t tat = (uint32_t)trow * kStep + (uint32_t)((q ^ L::key(trow)) * 16);
     auto sub = [](int s) { return (uint32_t)(kSwiglu ? (s >> 1) * 128 + (s & 1) * 32 : s * 32) * kStep; };
 
     Operands<TS> op[2];
-    // operand i of the step in `stage`, weights and rows of the first half first
+    // operand i of the step in `stage`, weights and rows of a part after another
     auto fetch = [&](Operands<TS>& o, int i, int stage) {
         const uint8_t* base = lds + stage * stage_bytes(TS);
-        const int half = i / (kSubs + TS), k = i % (kSubs + TS);
+        const int part = i / (kSubs + TS), k = i % (kSubs + TS);
         if (k < kSubs)
-            o.w[k][half] = *reinterpret_cast<const i32x4*>(base + (half ? wat ^ 32 : wat) + sub(k));
+            o.w[k][part] = *reinterpret_cast<const i32x4*>(base + (wat ^ part * 32) + sub(k));
         else
-            o.t[k - kSubs][half] = *reinterpret_cast<const i32x4*>(
-                base + (half ? tat ^ 32 : tat) + (k - kSubs) * 32 * kStep);
+            o.t[k - kSubs][part] = *reinterpret_cast<const i32x4*>(
+                base + (tat ^ part * 32) + (k - kSubs) * 32 * kStep);
     };
-    constexpr int kFetches = 2 * (kSubs + TS);
-    constexpr int kProducts = 2 * kSubs * TS;
+    constexpr int kFetches = kParts * (kSubs + TS);
+    constexpr int kProducts = kParts * kSubs * TS;
 
     phase_end<(S - 1) * L::kAll>();
 #pragma unroll
@@ -209,8 +213,8 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
         const int next = stage + 1 == S ? 0 : stage + 1;
 #pragma unroll
         for (int p = 0; p < kProducts; ++p) {
-            const int half = p / (kSubs * TS), m = p / kSubs % TS, s = p % kSubs;
-            acc[m][s] = __builtin_amdgcn_mfma_i32_32x32x32_i8(now.w[s][half], now.t[m][half],
+            const int part = p / (kSubs * TS), m = p / kSubs % TS, s = p % kSubs;
+            acc[m][s] = __builtin_amdgcn_mfma_i32_32x32x32_i8(now.w[s][part], now.t[m][part],
                                                               acc[m][s], 0, 0, 0);
             // its share of the next step's operands, in the first half of the
             // products, and of the loads
@@ -376,12 +380,13 @@ block_gemm_kernel(GemmArgs a)
     look_up(tile, s_tile[0]);
     __syncthreads();
     Tile t = read_tile(s_tile[0]);
-    const int nk = ((a.k + kStep - 1) / kStep + 1) & ~1;  // steps, in pairs
     bool loading = false;  // t's first slices are on their way
     int slot = 0;          // of the tile and its scales
     // One tile of class TS; then t is the next one (or has no rows).
     auto run = [&](auto ts) {
         constexpr int TS = decltype(ts)::value;
+        constexpr int kStep = step_bytes(TS);
+        const int nk = ((a.k + kStep - 1) / kStep + 1) & ~1;  // steps, in pairs
         const Loads<TS, kSwiglu> ld(a, t, lds0);
         if (!loading) {
             // loads past the end of a tile of another class may still write
