@@ -15,13 +15,14 @@
 // rows, each with up to 128 x 128 sums in registers: the fewest reads of LDS a
 // product (a wave of 128 x 64 would read 1.5 times as much, which with the
 // loads' writes is all that LDS can do while the matrix units are busy). For
-// each 64 or 128 elements of k (a step) the block holds both operands' slices in LDS,
-// loaded there directly from memory several steps before; a wave reads a
-// step's operands to registers during the step before, between the products.
-// One barrier a step: it says that the next step's slices are there and that
-// this step's, now in registers, may be overwritten.
+// each 128 elements of k (a step) the block holds both operands' slices in LDS,
+// loaded there directly from memory a step or two before; a wave reads half a
+// step's operands to registers while it multiplies the half before. One
+// barrier a step. A load takes whole cache lines: with 64 elements a step, half
+// a line a request, 256 experts x 32 rows (k 2048, n 7168) took 1130 us
+// instead of 750.
 //
-// LDS slices are 64 or 128 bytes a row without padding; the 16-byte chunks of a
+// LDS slices are 128 bytes a row without padding; the 16-byte chunks of a
 // row are permuted by a key of the row, so that the rows a matrix operand reads
 // together fall in different banks. The matrix instruction,
 // v_mfma_i32_32x32x32_i8, has the weights as its rows and the token rows as
@@ -48,13 +49,12 @@ constexpr int kSubs = 4;      // operands of 32 weight rows a wave
 constexpr int kMaxTS = 4;     // a tile of class TS has 64 TS rows
 constexpr int kTileRows = 64 * kMaxTS;
 
-// Bytes of k a step: 128, whole cache lines of a row, where that leaves room for
-// three slices; else 64.
-constexpr int step_bytes(int ts) { return ts <= 2 ? 128 : 64; }
-constexpr int a_bytes(int ts) { return 64 * ts * step_bytes(ts); }
-constexpr int stage_bytes(int ts) { return a_bytes(ts) + kTileN * step_bytes(ts); }
+constexpr int kStep = 128;    // bytes of k a step: whole cache lines of a row
+constexpr int kChunks = kStep / 16;
+constexpr int a_bytes(int ts) { return 64 * ts * kStep; }
+constexpr int stage_bytes(int ts) { return a_bytes(ts) + kTileN * kStep; }
 // Slices held: as many as fit.
-constexpr int stages(int ts) { return ts == 4 ? 4 : ts == 3 ? 5 : 3; }
+constexpr int stages(int ts) { return ts <= 2 ? 3 : 2; }
 constexpr int kScaleBytes = (kTileRows + kTileN) * 4;
 constexpr int kScales = 144 * 1024;  // their place
 static_assert(stages(4) * stage_bytes(4) <= kScales && stages(3) * stage_bytes(3) <= kScales &&
@@ -70,35 +70,29 @@ struct Tile {
     int col;        // column tile
 };
 
-// The loads of a tile. A wave's i-th 1 KB of a slice holds rows kRows * (4 * i +
-// wave) .. of kRows, a lane one 16-byte chunk of a row. Chunks past k are asked
+// Place of a row's 16-byte chunk in its slice: exclusive-or with this. The 16
+// rows that an operand reads together (lanes 0-3, 12-15, 20-27 of 32, and the
+// others) lie in different banks so, of 64 (measured: no conflicts).
+__device__ __forceinline__ int key(int row) { return (row >> 1) & (kChunks - 1); }
+
+// The loads of a tile. A wave's i-th 1 KB of a slice holds rows 8 * (4 * i +
+// wave) .. of 8, a lane one 16-byte chunk of a row. Chunks past k are asked
 // for too, from beyond the resource's end (zeros, without memory traffic), so
 // that every step has the same loads in flight and no branch.
 // kSwiglu: weight rows [0, 128) of the tile are gate rows 128 * col .., rows
 // [128, 256) the up rows. Otherwise they are rows 256 * col .. .
 template <int TS, bool kSwiglu>
 struct Loads {
-    static constexpr int kStep = step_bytes(TS);
-    static constexpr int kChunks = kStep / 16;          // of a row
-    static constexpr int kRows = kWave / kChunks;       // of a load
-    static constexpr int kALoads = 64 * TS / (4 * kRows);
-    static constexpr int kBLoads = kTileN / (4 * kRows);
-    static constexpr int kAll = kALoads + kBLoads;      // a wave and step
+    static constexpr int kALoads = 2 * TS;
+    static constexpr int kBLoads = 8;
+    static constexpr int kAll = kALoads + kBLoads;  // a wave and step
     u32x4 ra, rb0, rb1;                        // rows, the two halves of the weights
     u32x4 ras, rbs;                            // the rows' scales, this wave's weight rows'
     uint32_t off;                              // of this lane's chunk of the load's first rows
     int left;                                  // bytes of k from this lane's chunk on
-    uint32_t rows4;                            // bytes of a load's rows of k, times 4
+    uint32_t rows32;                           // bytes of 32 rows of k
     uint32_t lds0;
     int wave;
-
-    // Place of a row's chunk: exclusive-or with it. The 16 rows that an operand
-    // reads together (lanes 0-3, 12-15, 20-27 of 32, and the others) lie in
-    // different banks so, of 64.
-    static __device__ __forceinline__ int key(int row)
-    {
-        return (row / (256 / kStep)) & (kChunks - 1);
-    }
 
     __device__ __forceinline__ Loads(const GemmArgs& a, const Tile& t, uint32_t block_lds0)
         : lds0(block_lds0)
@@ -106,10 +100,8 @@ struct Loads {
         const int lane = threadIdx.x & (kWave - 1);
         wave = uniform(threadIdx.x / kWave);
         const uint32_t K = (uint32_t)a.k;
-        const int lr = wave * kRows + lane / kChunks;  // row of i = 0; i adds 4 kRows
-        rows4 = 4 * kRows * K;
-        static_assert(4 * kRows * kStep % 256 == 0 && (4 * kRows * kStep / 256) % kChunks == 0,
-                      "the key of a load's rows does not depend on i");
+        const int lr = wave * 8 + lane / kChunks;  // row of i = 0; i adds 32
+        rows32 = 32 * K;
         const int chunk = (lane & (kChunks - 1)) ^ key(lr);
         off = (uint32_t)lr * K + (uint32_t)chunk * 16u;
         left = a.k - chunk * 16;
@@ -134,11 +126,11 @@ struct Loads {
         const uint32_t dst = lds0 + stage * stage_bytes(TS) + i * 4096 + wave * 1024;
         constexpr int kHalf = kBLoads / 2;
         if (i < kALoads)
-            load_to_lds<false>(ra, dst, at + i * rows4, (uint32_t)h * kStep);
+            load_to_lds<false>(ra, dst, at + i * rows32, (uint32_t)h * kStep);
         else if (i < kALoads + kHalf)
-            load_to_lds<(TS < kMaxTS)>(rb0, dst, at + (i - kALoads) * rows4, (uint32_t)h * kStep);
+            load_to_lds<(TS < kMaxTS)>(rb0, dst, at + (i - kALoads) * rows32, (uint32_t)h * kStep);
         else
-            load_to_lds<(TS < kMaxTS)>(rb1, dst, at + (i - kALoads - kHalf) * rows4,
+            load_to_lds<(TS < kMaxTS)>(rb1, dst, at + (i - kALoads - kHalf) * rows32,
                                        (uint32_t)h * kStep);
     }
 
@@ -157,20 +149,23 @@ struct Loads {
     }
 };
 
-// A wave's operands of one step: 32 bytes of k each.
+// A wave's operands of half a step: 32 bytes of k, twice.
 template <int TS>
 struct Operands {
-    static constexpr int kParts = step_bytes(TS) / 32;
-    i32x4 w[kSubs][kParts], t[TS][kParts];
+    i32x4 w[kSubs][2], t[TS][2];
 };
 
-// The sums of one tile, whose first slices are on their way.
+// The sums of one tile, whose first slices are on their way. A step's first
+// half multiplies while the second half's operands are read; then a barrier
+// says that every wave has them, so that the step's place is free for the
+// slice `stages` further, and that the next step's slice is there, from which
+// the second half reads.
 template <int TS, bool kSwiglu>
 __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uint8_t* lds, int nk,
                                          i32x16 (&acc)[TS][kSubs])
 {
     using L = Loads<TS, kSwiglu>;
-    constexpr int S = stages(TS), kStep = L::kStep, kParts = Operands<TS>::kParts;
+    constexpr int S = stages(TS);
     const int lane = threadIdx.x & (kWave - 1);
     const int wm = ld.wave >> 1, wn = ld.wave & 1;
     const int q = lane >> 5, i32 = lane & 31;
@@ -178,29 +173,51 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
     // the result, which holds rows 8 b + 4 q + t, b and t 0 .. 3
     const int b = i32 >> 3, j = (b >> 1) * 16 + ((i32 >> 2) & 1) * 8 + (b & 1) * 4 + (i32 & 3);
     const int wrow = wn * (kSwiglu ? 64 : 128) + j;
-    const uint32_t wat = a_bytes(TS) + (uint32_t)wrow * kStep + (uint32_t)((q ^ L::key(wrow)) * 16);
+    const uint32_t wat = a_bytes(TS) + (uint32_t)wrow * kStep + (uint32_t)((q ^ key(wrow)) * 16);
     const int trow = wm * 32 * TS + i32;
-    const uint32_t tat = (uint32_t)trow * kStep + (uint32_t)((q ^ L::key(trow)) * 16);
-    auto sub = [](int s) { return (uint32_t)(kSwiglu ? (s >> 1) * 128 + (s & 1) * 32 : s * 32) * kStep; };
+    const uint32_t tat = (uint32_t)trow * kStep + (uint32_t)((q ^ key(trow)) * 16);
+    auto sub = [](int s) {
+        return (uint32_t)(kSwiglu ? (s >> 1) * 128 + (s & 1) * 32 : s * 32) * kStep;
+    };
 
     Operands<TS> op[2];
-    // operand i of the step in `stage`, weights and rows of a part after another
-    auto fetch = [&](Operands<TS>& o, int i, int stage) {
+    constexpr int kFetches = 2 * (kSubs + TS);
+    constexpr int kProducts = 2 * kSubs * TS;
+    // operand i of a half of the step in `stage`, weights, then rows
+    auto fetch = [&](int half, int i, int stage) {
         const uint8_t* base = lds + stage * stage_bytes(TS);
-        const int part = i / (kSubs + TS), k = i % (kSubs + TS);
+        const int part = i / (kSubs + TS), k = i % (kSubs + TS), c = half * 64 + part * 32;
         if (k < kSubs)
-            o.w[k][part] = *reinterpret_cast<const i32x4*>(base + (wat ^ part * 32) + sub(k));
+            op[half].w[k][part] = *reinterpret_cast<const i32x4*>(base + (wat ^ c) + sub(k));
         else
-            o.t[k - kSubs][part] = *reinterpret_cast<const i32x4*>(
-                base + (tat ^ part * 32) + (k - kSubs) * 32 * kStep);
+            op[half].t[k - kSubs][part] = *reinterpret_cast<const i32x4*>(
+                base + (tat ^ c) + (k - kSubs) * 32 * kStep);
     };
-    constexpr int kFetches = kParts * (kSubs + TS);
-    constexpr int kProducts = kParts * kSubs * TS;
+    // the products of a half, with `more(p)` after each
+    auto products = [&](int half, auto more) {
+#pragma unroll
+        for (int p = 0; p < kProducts; ++p) {
+            const int part = p / (kSubs * TS), m = p / kSubs % TS, s = p % kSubs;
+            acc[m][s] = __builtin_amdgcn_mfma_i32_32x32x32_i8(op[half].w[s][part],
+                                                              op[half].t[m][part], acc[m][s], 0, 0,
+                                                              0);
+            more(p);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // this product's share of the other half's operands: all of them in the
+    // first half of the products
+    auto fetches = [&](int p, int half, int stage) {
+#pragma unroll
+        for (int i = 2 * p * kFetches / kProducts;
+             i < 2 * (p + 1) * kFetches / kProducts && i < kFetches; ++i)
+            fetch(half, i, stage);
+    };
 
     phase_end<(S - 1) * L::kAll>();
 #pragma unroll
     for (int i = 0; i < kFetches; ++i)
-        fetch(op[0], i, 0);
+        fetch(0, i, 0);
 #pragma unroll
     for (int m = 0; m < TS; ++m)
 #pragma unroll
@@ -208,30 +225,18 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
             acc[m][s] = i32x16{};
 
     int stage = 0;
-    auto step = [&](int h, Operands<TS>& now, Operands<TS>& then) {
-        phase_end<(S - 2) * L::kAll>();
+    for (int h = 0; h < nk; ++h) {
         const int next = stage + 1 == S ? 0 : stage + 1;
+        products(0, [&](int p) { fetches(p, 1, stage); });
+        phase_end<(S - 2) * L::kAll>();
+        products(1, [&](int p) {
+            fetches(p, 0, next);
 #pragma unroll
-        for (int p = 0; p < kProducts; ++p) {
-            const int part = p / (kSubs * TS), m = p / kSubs % TS, s = p % kSubs;
-            acc[m][s] = __builtin_amdgcn_mfma_i32_32x32x32_i8(now.w[s][part], now.t[m][part],
-                                                              acc[m][s], 0, 0, 0);
-            // its share of the next step's operands, in the first half of the
-            // products, and of the loads
-#pragma unroll
-            for (int i = 2 * p * kFetches / kProducts;
-                 i < 2 * (p + 1) * kFetches / kProducts && i < kFetches; ++i)
-                fetch(then, i, next);
-#pragma unroll
-            for (int i = p * L::kAll / kProducts; i < (p + 1) * L::kAll / kProducts; ++i)
+            for (int i = 2 * p * L::kAll / kProducts;
+                 i < 2 * (p + 1) * L::kAll / kProducts && i < L::kAll; ++i)
                 ld.load(i, h + S, stage);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        });
         stage = next;
-    };
-    for (int h = 0; h < nk; h += 2) {
-        step(h, op[0], op[1]);
-        step(h + 1, op[1], op[0]);
     }
     phase_end();
 }
@@ -380,13 +385,12 @@ block_gemm_kernel(GemmArgs a)
     look_up(tile, s_tile[0]);
     __syncthreads();
     Tile t = read_tile(s_tile[0]);
+    const int nk = (a.k + kStep - 1) / kStep;  // steps
     bool loading = false;  // t's first slices are on their way
     int slot = 0;          // of the tile and its scales
     // One tile of class TS; then t is the next one (or has no rows).
     auto run = [&](auto ts) {
         constexpr int TS = decltype(ts)::value;
-        constexpr int kStep = step_bytes(TS);
-        const int nk = ((a.k + kStep - 1) / kStep + 1) & ~1;  // steps, in pairs
         const Loads<TS, kSwiglu> ld(a, t, lds0);
         if (!loading) {
             // loads past the end of a tile of another class may still write
