@@ -55,6 +55,7 @@ constexpr int a_bytes(int ts) { return 64 * ts * kStep; }
 constexpr int stage_bytes(int ts) { return a_bytes(ts) + kTileN * kStep; }
 // Slices held: as many as fit.
 constexpr int stages(int ts) { return ts <= 2 ? 3 : 2; }
+constexpr int kHeldGroups = 1024;  // whose row counts are kept in LDS
 constexpr int kScaleBytes = (kTileRows + kTileN) * 4;
 constexpr int kScales = 144 * 1024;  // their place
 static_assert(stages(4) * stage_bytes(4) <= kScales && stages(3) * stage_bytes(3) <= kScales &&
@@ -232,8 +233,7 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
         products(1, [&](int p) {
             fetches(p, 0, next);
 #pragma unroll
-            for (int i = 2 * p * L::kAll / kProducts;
-                 i < 2 * (p + 1) * L::kAll / kProducts && i < L::kAll; ++i)
+            for (int i = p * L::kAll / kProducts; i < (p + 1) * L::kAll / kProducts; ++i)
                 ld.load(i, h + S, stage);
         });
         stage = next;
@@ -298,15 +298,22 @@ block_gemm_kernel(GemmArgs a)
     __shared__ int s_part[kThreads / kWave];
     __shared__ int s_first[kThreads + 1];
     __shared__ int s_tile[2][4];
+    __shared__ int s_rows[kHeldGroups];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
 
     // Row tiles of each thread's share of the groups, as where they start in
-    // the list of all (group after group).
-    auto rows_of = [&](int g) {
+    // the list of all (group after group). Row counts of the first groups are
+    // kept in LDS: a look at memory between tiles would wait for every load and
+    // store before it.
+    auto count_of = [&](int g) {
         return a.counts ? max(0, min(a.counts[g], a.cap)) : a.cap;
     };
+    auto rows_of = [&](int g) { return g < kHeldGroups ? s_rows[g] : count_of(g); };
+    for (int g = threadIdx.x; g < min(a.groups, kHeldGroups); g += kThreads)
+        s_rows[g] = count_of(g);
+    __syncthreads();
     const int share = (a.groups + kThreads - 1) / kThreads;
     {
         const int g0 = min(a.groups, (int)threadIdx.x * share), g1 = min(a.groups, g0 + share);
