@@ -239,6 +239,24 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
         stage = next;
     }
     phase_end();
+    // the last products' results, before sum() reads them: a read may not
+    // follow a product of 16 passes within 18 issue slots
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A sum, out of the accumulation registers. In assembly because the compiler
+// would move all 256 to the other registers at once, and those of the next
+// tile's addresses to memory.
+__device__ __forceinline__ int sum(int a)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    int v;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+    return v;
+#else
+    return a;
+#endif
 }
 
 // The tile's sums to memory.
@@ -276,9 +294,10 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, const u
                 float f[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    f[r] = sa * (cs[r] * (float)acc[m][s][h * 8 + r]);
+                    f[r] = sa * (cs[r] * (float)sum(acc[m][s][h * 8 + r]));
                     if constexpr (kSwiglu)
-                        f[r] = silu_times(f[r], sa * (us[r] * (float)acc[m][s + kCols][h * 8 + r]));
+                        f[r] = silu_times(
+                            f[r], sa * (us[r] * (float)sum(acc[m][s + kCols][h * 8 + r])));
                 }
                 if (col < width)  // rows past the tile's are dropped by the resource
                     bstore16<0>(narrow<DT>(f), ro,
