@@ -150,6 +150,54 @@ struct Loads {
     }
 };
 
+// A tile's stores: of each 8 columns of a lane's rows. The first kNow are made
+// at the tile's end, the others, kEach at a time, in the first kDelay steps of
+// the next tile: a wave's waits are in order, so that one for a load waits for
+// the stores before it too, and a whole tile's at once take long.
+template <int TS, bool kSwiglu>
+struct Stores {
+    static constexpr int kCols = kSwiglu ? kSubs / 2 : kSubs;  // operands of columns
+    static constexpr int kAll = 2 * kCols * TS;
+    static constexpr int kDelay = 4;
+    static constexpr int kHeld = kAll < 16 ? kAll : 16;        // (64 registers)
+    static constexpr int kEach = kHeld / kDelay;
+    static constexpr int kNow = kAll - kHeld;
+    static_assert(kHeld % kDelay == 0, "whole steps");
+
+    u32x4 held[kHeld];
+    u32x4 words;      // of the resource over the tile's rows
+    uint32_t off;     // of this lane's first column in its first row
+    int left;         // columns from there to the row's end
+    uint32_t rows32;  // bytes of 32 rows
+
+    __device__ __forceinline__ Stores() : words{}, off(0), left(0), rows32(0)
+    {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            held[i] = u32x4{};
+    }
+
+    // Store i is of columns 16 (i / TS) and rows 32 (i % TS) from the first on.
+    __device__ __forceinline__ void store(int i, const u32x4& v) const
+    {
+        const int col = i / TS * 16;
+        const uint32_t lo = words[0], hi = words[1], at = off + i % TS * rows32 + col * 2;
+        // rows past the tile's (and all without a tile) are dropped by the resource
+        bstore16<0>(v, row_rsrc(reinterpret_cast<const void*>(lo | (uint64_t)hi << 32), words[2]),
+                    col < left ? at : 1u << 31);
+    }
+
+    __device__ __forceinline__ void later(int i) const { store(kNow + i, held[i]); }
+
+    __device__ __forceinline__ void rest(int from) const
+    {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (i >= from)
+                later(i);
+    }
+};
+
 // A wave's operands of half a step: 32 bytes of k, twice.
 template <int TS>
 struct Operands {
@@ -163,9 +211,11 @@ struct Operands {
 // the second half reads.
 template <int TS, bool kSwiglu>
 __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uint8_t* lds, int nk,
+                                         const Stores<TS, kSwiglu>& stores,
                                          i32x16 (&acc)[TS][kSubs])
 {
     using L = Loads<TS, kSwiglu>;
+    using St = Stores<TS, kSwiglu>;
     constexpr int S = stages(TS);
     const int lane = threadIdx.x & (kWave - 1);
     const int wm = ld.wave >> 1, wn = ld.wave & 1;
@@ -215,7 +265,7 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
             fetch(half, i, stage);
     };
 
-    phase_end<(S - 1) * L::kAll>();
+    phase_end<(S - 1) * L::kAll + St::kNow>();
 #pragma unroll
     for (int i = 0; i < kFetches; ++i)
         fetch(0, i, 0);
@@ -226,10 +276,23 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
             acc[m][s] = i32x16{};
 
     int stage = 0;
-    for (int h = 0; h < nk; ++h) {
+    // Step h. D: h up to kDelay, whose stores come with it. In flight at its
+    // barrier at most what was asked for after the loads of step h + 1: those
+    // of the steps after it, and stores: these are one or two steps' (S - 1),
+    // and the last tile's immediate ones as long as the loads are older.
+    auto step = [&](int h, auto d) {
+        constexpr int D = decltype(d)::value;
+        constexpr int kEach = D < St::kDelay ? St::kEach : 0;
+        constexpr int kBefore = S > 2 && D > 0 && D <= St::kDelay ? St::kEach : 0;
+        constexpr int kFirst = D < S - 1 ? St::kNow : 0;
         const int next = stage + 1 == S ? 0 : stage + 1;
-        products(0, [&](int p) { fetches(p, 1, stage); });
-        phase_end<(S - 2) * L::kAll>();
+        products(0, [&](int p) {
+            fetches(p, 1, stage);
+#pragma unroll
+            for (int i = p * kEach / kProducts; i < (p + 1) * kEach / kProducts; ++i)
+                stores.later(D * St::kEach + i);
+        });
+        phase_end<(S - 2) * L::kAll + kEach + kBefore + kFirst>();
         products(1, [&](int p) {
             fetches(p, 0, next);
 #pragma unroll
@@ -237,7 +300,22 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
                 ld.load(i, h + S, stage);
         });
         stage = next;
-    }
+    };
+    static_assert(St::kDelay == 4, "the steps below");
+    step(0, std::integral_constant<int, 0>());
+    if (nk > 1)
+        step(1, std::integral_constant<int, 1>());
+    if (nk > 2)
+        step(2, std::integral_constant<int, 2>());
+    if (nk > 3)
+        step(3, std::integral_constant<int, 3>());
+    else  // (from a constant, so that the held ones stay in registers)
+        nk == 3 ? stores.rest(3 * St::kEach) : nk == 2 ? stores.rest(2 * St::kEach)
+                                                       : stores.rest(St::kEach);
+    if (nk > 4)
+        step(4, std::integral_constant<int, 4>());
+    for (int h = 5; h < nk; ++h)
+        step(h, std::integral_constant<int, 5>());
     phase_end();
     // the last products' results, before sum() reads them: a read may not
     // follow a product of 16 passes within 18 issue slots
@@ -259,11 +337,12 @@ __device__ __forceinline__ int sum(int a)
 #endif
 }
 
-// The tile's sums to memory.
+// The tile's sums to memory, or to `stores` for later.
 template <int TS, int DT, bool kSwiglu>
 __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, const uint8_t* scales,
-                                       i32x16 (&acc)[TS][kSubs])
+                                       i32x16 (&acc)[TS][kSubs], Stores<TS, kSwiglu>& stores)
 {
+    using St = Stores<TS, kSwiglu>;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
     const int wm = wave >> 1, wn = wave & 1, q = lane >> 5;
@@ -271,38 +350,36 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, const u
     const float* bs = as + kTileRows;
     const int width = kSwiglu ? a.n / 2 : a.n;
     const int trow = wm * 32 * TS + (lane & 31);
-    const __amdgpu_buffer_rsrc_t ro =
-        uniform_rsrc(a.out + t.row0 * width * 2, (int64_t)t.rows * width * 2);
-    constexpr int kCols = kSwiglu ? kSubs / 2 : kSubs;
-    const int wcol = wn * kCols * 32;
+    const int wcol = wn * St::kCols * 32 + q * 8;       // in the tile
+    const int col = t.col * (kSwiglu ? 128 : kTileN) + wcol;
+    stores.words = rsrc_words(a.out + t.row0 * width * 2, t.rows * width * 2);
+    stores.off = ((uint32_t)trow * (uint32_t)width + (uint32_t)col) * 2u;
+    stores.left = width - col;
+    stores.rows32 = 64u * (uint32_t)width;
 #pragma unroll
-    for (int s = 0; s < kCols; ++s) {
+    for (int s = 0; s < 2 * St::kCols; ++s) {  // runs of 8 columns, 16 apart
+        float cs[8], us[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // runs of 8 columns
-            const int j = wcol + s * 32 + h * 16 + q * 8;       // in the tile
-            const int col = t.col * (kSwiglu ? 128 : kTileN) + j;
-            float cs[8], us[8];
+        for (int r = 0; r < 8; ++r) {
+            cs[r] = bs[wcol + s * 16 + r];
+            us[r] = kSwiglu ? bs[128 + wcol + s * 16 + r] : 0.0f;
+        }
+#pragma unroll
+        for (int m = 0; m < TS; ++m) {
+            const float sa = as[trow + m * 32];
+            float f[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                cs[r] = bs[j + r];
-                us[r] = kSwiglu ? bs[128 + j + r] : 0.0f;
+                f[r] = sa * (cs[r] * (float)sum(acc[m][s / 2][s % 2 * 8 + r]));
+                if constexpr (kSwiglu)
+                    f[r] = silu_times(
+                        f[r], sa * (us[r] * (float)sum(acc[m][s / 2 + St::kCols][s % 2 * 8 + r])));
             }
-#pragma unroll
-            for (int m = 0; m < TS; ++m) {
-                const int row = trow + m * 32;
-                const float sa = as[row];
-                float f[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    f[r] = sa * (cs[r] * (float)sum(acc[m][s][h * 8 + r]));
-                    if constexpr (kSwiglu)
-                        f[r] = silu_times(
-                            f[r], sa * (us[r] * (float)sum(acc[m][s + kCols][h * 8 + r])));
-                }
-                if (col < width)  // rows past the tile's are dropped by the resource
-                    bstore16<0>(narrow<DT>(f), ro,
-                                ((uint32_t)row * (uint32_t)width + (uint32_t)col) * 2u);
-            }
+            const int i = s * TS + m;
+            if (i < St::kNow)
+                stores.store(i, narrow<DT>(f));
+            else
+                stores.held[i - St::kNow] = narrow<DT>(f);
         }
     }
 }
@@ -412,38 +489,35 @@ block_gemm_kernel(GemmArgs a)
     __syncthreads();
     Tile t = read_tile(s_tile[0]);
     const int nk = (a.k + kStep - 1) / kStep;  // steps
-    bool loading = false;  // t's first slices are on their way
-    int slot = 0;          // of the tile and its scales
-    // One tile of class TS; then t is the next one (or has no rows).
+    int slot = 0;  // of the tile and its scales
+    // Tiles of class TS, as long as the next one is of it; then t is the next
+    // one (or has no rows).
     auto run = [&](auto ts) {
         constexpr int TS = decltype(ts)::value;
-        const Loads<TS, kSwiglu> ld(a, t, lds0);
-        if (!loading) {
-            // loads past the end of a tile of another class may still write
-            phase_end<0>();
-            ld.prologue(slot);
+        Stores<TS, kSwiglu> stores;
+        // loads past the end of a tile of another class may still write
+        phase_end<0>();
+        Loads<TS, kSwiglu>(a, t, lds0).prologue(slot);
+        bool more = true;
+        while (more) {
+            t0 += gridDim.x;
+            const int64_t next = tile_at(t0);
+            if (next >= 0)
+                look_up(next, s_tile[slot ^ 1]);  // read after the steps' barriers
+            i32x16 acc[TS][kSubs];
+            multiply<TS, kSwiglu>(Loads<TS, kSwiglu>(a, t, lds0), lds, nk, stores, acc);
+            const Tile done = t;
+            const uint8_t* scales = lds + kScales + slot * kScaleBytes;
+            slot ^= 1;
+            t.rows = 0;
+            if (next >= 0)
+                t = read_tile(s_tile[slot]);
+            more = t.rows > 0 && tile_class(t.rows) == TS;
+            if (more)  // the next tile's first loads
+                Loads<TS, kSwiglu>(a, t, lds0).prologue(slot);
+            finish<TS, DT, kSwiglu>(a, done, scales, acc, stores);
         }
-        t0 += gridDim.x;
-        const int64_t next = tile_at(t0);
-        if (next >= 0)
-            look_up(next, s_tile[slot ^ 1]);  // read after the steps' barriers
-        i32x16 acc[TS][kSubs];
-        multiply<TS, kSwiglu>(ld, lds, nk, acc);
-        const Tile done = t;
-        const uint8_t* scales = lds + kScales + slot * kScaleBytes;
-        slot ^= 1;
-        t.rows = 0;
-        loading = false;
-        if (next >= 0) {
-            t = read_tile(s_tile[slot]);
-            if (tile_class(t.rows) == TS) {
-                // the next tile's loads run under this one's stores
-                const Loads<TS, kSwiglu> then(a, t, lds0);
-                then.prologue(slot);
-                loading = true;
-            }
-        }
-        finish<TS, DT, kSwiglu>(a, done, scales, acc);
+        stores.rest(0);
     };
     while (t.rows > 0) {
         switch (tile_class(t.rows)) {
