@@ -26,7 +26,7 @@
 
 #include <type_traits>
 
-#include "block_device.h"
+#include "block_lds.h"
 
 namespace block {
 namespace {
@@ -43,6 +43,7 @@ constexpr int kDownWaves = 8;
 constexpr int kMaxWords = kFewMaxExperts / 32;
 constexpr int kBlockK = 128;  // elements of k a step
 constexpr uint32_t kNowhere = 1u << 31;
+constexpr size_t kFewLds = 160 * 1024;  // of a compute unit
 
 // 4 codes as 4 values of the tokens' type (XT 0 bf16, 1 fp16), exact. WT: 0
 // E4M3, 1 int8.
@@ -95,26 +96,77 @@ __device__ __forceinline__ f32x4 product(const u32x4& w, const u32x4& x, const f
                                                       __builtin_bit_cast(f16x8, x), c, 0, 0, 0);
 }
 
-// What a block knows of the routing: the expert of each slot that is its
-// token's first to name it (else -1), and the experts hit, by their number.
+// What a call's routing comes to: the expert of each slot that is its token's
+// first to name it (else -1), and the experts hit, each once, in any order.
+//
+// Of up to 64 slots a wave knows it by itself, one slot a lane, without a
+// barrier: a loop over the experts hit.
+struct WaveRouting {
+    int id;           // of this lane's slot, if it is its token's first of its expert
+    uint64_t firsts;  // lanes that are the call's first of their expert
+    int hits;
+
+    __device__ __forceinline__ explicit WaveRouting(const FewArgs& a)
+    {
+        const int lane = threadIdx.x & (kWave - 1), P = a.T * a.topk;
+        const int raw = lane < P ? a.ids[lane] : -1;
+        const bool valid = raw >= 0 && raw < a.E;
+        const uint64_t below = (1ull << lane) - 1;                // lanes below this one
+        const uint64_t others = (1ull << (lane - lane % a.topk)) - 1;  // of tokens before
+        uint64_t left = __ballot(valid);
+        id = -1;
+        firsts = 0;
+        hits = 0;
+        while (left) {
+            const int first = (int)__builtin_ctzll(left);
+            const int e = __builtin_amdgcn_readlane(raw, first);
+            const uint64_t m = __ballot(valid && raw == e);
+            if (raw == e && valid && !(m & below & ~others))
+                id = e;
+            firsts |= 1ull << first;
+            left &= ~m;
+            ++hits;
+        }
+    }
+
+    // The u-th expert: its first lane in the call is its token's first too.
+    __device__ __forceinline__ int expert(int u) const
+    {
+        const int lane = threadIdx.x & (kWave - 1);
+        const bool yes = (firsts >> lane & 1) && lanes_below(firsts) == u;
+        return __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(__ballot(yes)));
+    }
+
+    // The slots of expert e that are their token's first of it, in order, to
+    // list; how many.
+    __device__ __forceinline__ int slots_of(const FewArgs&, int e, int* list) const
+    {
+        const uint64_t b = __ballot(id == e);
+        if (id == e)
+            list[lanes_below(b)] = threadIdx.x & (kWave - 1);
+        return (int)__popcll(b);
+    }
+};
+
+// Of more, a block works it out in LDS.
 struct Routing {
     int id[kFewMaxSlots];
     int hit[kFewMaxSlots];
-    uint32_t bits[kMaxWords];
     int part[16];
     int hits;
 };
 
-// Fills s in a block of N threads. Ends with a barrier.
+// Fills s in a block of N threads; bits: kMaxWords words of LDS, for the while.
+// Ends with a barrier.
 template <int N>
-__device__ __forceinline__ void read_routing(const FewArgs& a, Routing& s)
+__device__ __forceinline__ void read_routing(const FewArgs& a, Routing& s, uint32_t* bits)
 {
     const int tid = threadIdx.x, P = a.T * a.topk;
     const int words = (a.E + 31) / 32;
     for (int p = tid; p < P; p += N)
         s.hit[p] = a.ids[p];  // (as they come; the list of hits is made later)
     for (int i = tid; i < words; i += N)
-        s.bits[i] = 0;
+        bits[i] = 0;
     __syncthreads();
     for (int p = tid; p < P; p += N) {
         const int e = s.hit[p], first = p - p % a.topk;
@@ -123,14 +175,14 @@ __device__ __forceinline__ void read_routing(const FewArgs& a, Routing& s)
             lead = lead && s.hit[j] != e;
         s.id[p] = lead ? e : -1;
         if (lead)
-            atomicOr(&s.bits[e >> 5], 1u << (e & 31));
+            atomicOr(&bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
     const int share = (words + N - 1) / N;
     const int w0 = min(words, tid * share), w1 = min(words, w0 + share);
     int mine = 0;
     for (int i = w0; i < w1; ++i)
-        mine += __popc(s.bits[i]);
+        mine += __popc(bits[i]);
     int inc = mine;
     const int lane = tid & (kWave - 1), wave = tid / kWave;
 #pragma unroll
@@ -149,113 +201,230 @@ __device__ __forceinline__ void read_routing(const FewArgs& a, Routing& s)
         total += s.part[w];
     }
     for (int i = w0; i < w1; ++i)
-        for (uint32_t b = s.bits[i]; b; b &= b - 1)
+        for (uint32_t b = bits[i]; b; b &= b - 1)
             s.hit[at++] = i * 32 + __ffs(b) - 1;
     if (tid == 0)
         s.hits = total;
     __syncthreads();
 }
 
-// The slots of expert e, in order, to list; how many. One wave.
-__device__ __forceinline__ int slots_of(const Routing& s, int P, int e, int* list)
-{
-    const int lane = threadIdx.x & (kWave - 1);
-    int n = 0;
-    for (int p0 = 0; p0 < P; p0 += kWave) {
-        const int p = p0 + lane;
-        const bool yes = p < P && s.id[p] == e;
-        const uint64_t b = __ballot(yes);
-        if (yes)
-            list[n + lanes_below(b)] = p;
-        n += (int)__popcll(b);
+struct BlockRouting {
+    Routing& s;
+    int hits;
+
+    __device__ __forceinline__ int expert(int u) const { return uniform(s.hit[u]); }
+
+    __device__ __forceinline__ int slots_of(const FewArgs& a, int e, int* list) const
+    {
+        const int lane = threadIdx.x & (kWave - 1), P = a.T * a.topk;
+        int n = 0;
+        for (int p0 = 0; p0 < P; p0 += kWave) {
+            const int p = p0 + lane;
+            const bool yes = p < P && s.id[p] == e;
+            const uint64_t b = __ballot(yes);
+            if (yes)
+                list[n + lanes_below(b)] = p;
+            n += (int)__popcll(b);
+        }
+        return n;
     }
-    return n;
+};
+
+// Calls f with the routing, known to every wave: of up to 64 slots (kSmall)
+// without a barrier. scratch: kMaxWords words of LDS that f may use again.
+template <bool kSmall, int N, class F>
+__device__ __forceinline__ void with_routing(const FewArgs& a, uint8_t* scratch, F&& f)
+{
+    if constexpr (kSmall) {
+        f(WaveRouting(a));
+    } else {
+        __shared__ Routing s;
+        read_routing<N>(a, s, reinterpret_cast<uint32_t*>(scratch));
+        f(BlockRouting{s, uniform(s.hits)});
+    }
 }
 
-// The sums over steps [k0, k1) of R operands of 16 weight rows with G groups of
-// 16 columns. rsrc[r]: resource of operand r's 16 rows of K bytes; xoff[g]:
-// byte offset of this lane's column (kNowhere: none) in X resources rx, of
-// which the operand of k is the sum (X = 2: values and their rests). scale(r,
-// step): operand r's scale of that step, of FP8 weights. D: steps in flight.
-template <int R, int G, int X, int WT, int XT, int D, class Scale>
-__device__ __forceinline__ void accumulate(const __amdgpu_buffer_rsrc_t (&rw)[R],
-                                           const __amdgpu_buffer_rsrc_t (&rx)[X],
-                                           const uint32_t (&xoff)[G], int K, int k0, int k1,
-                                           Scale&& scale, f32x4 (&acc)[R][G])
+// Each lane's value of the lane N further in its row of 16.
+template <int N>
+__device__ __forceinline__ u32x4 rotated(const u32x4& v)
 {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int q = lane >> 4;
-    const uint32_t woff = (uint32_t)(lane & 15) * (uint32_t)K + (uint32_t)q * 16u;
-    struct Step {
-        u32x4 w[R][2], x[G][X][4];
-    };
-    Step in[D];
-    auto load = [&](int k, Step& s) {
+    constexpr int kRowRotateRight = 0x120;
+    u32x4 r;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            // 16 elements of k: rows end at K, steps at k1
-            const int at = k * kBlockK + half * 64;
-            const bool there = k < k1 && at + q * 16 < K;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                s.w[r][half] = bload16<2>(rw[r], there ? woff + at : kNowhere);
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int v = 0; v < X; ++v)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        s.x[g][v][half * 2 + c] = bload16<0>(
-                            rx[v], there ? xoff[g] + (uint32_t)(at + q * 16 + c * 8) * 2u : kNowhere);
-        }
-    };
-    auto use = [&](int k, const Step& s) {
-        f32x4 sum[R][G];
+    for (int i = 0; i < 4; ++i) {
+        const int w = (int)v[i];
+        r[i] = (uint32_t)__builtin_amdgcn_update_dpp(w, w, kRowRotateRight + 16 - N, 0xF, 0xF, true);
+    }
+    return r;
+}
+
+// One wave's sums over steps [k0, k1) of R operands of 16 weight rows with up
+// to C columns, 4 or 16. The wave's own ring in LDS holds D steps' weights and
+// columns, loaded straight there, so that as much is in flight as there is LDS,
+// whatever the registers, and a load takes whole cache lines: 8 rows of 128
+// bytes (64 bytes of 16 rows, which is how the operands lie in registers, took
+// a fifth longer). Its chunks are permuted by the row, as the reads' banks want.
+// Up to 4 columns lie packed: lane 4 c + i of each 16 has what column i
+// multiplies with the step's operand c, one load a step instead of four, and a
+// rotation of the 16 lanes by 4 c puts it in place (columns 4 and up hold what
+// nobody reads).
+template <int R, int C, int X, int WT, int XT, int D>
+struct Sums {
+    static constexpr bool kPacked = C <= 4;
+    static constexpr int kXLoads = kPacked ? 1 : 4;  // a step and plane of columns
+    static constexpr int kAll = 2 * R + X * kXLoads;
+    static constexpr int kBytes = kAll * 1024;       // a step's
+
+    u32x4 rw[R], rx[X];  // resources: 16 rows of K bytes each; the planes of the columns
+    uint32_t lds0;       // of the ring
+    const uint8_t* lds;
+    uint32_t woff[2];    // this lane's chunk of the first step, in either 8 rows
+    uint32_t xoff;
+    int wleft[2], xleft; // elements of k from there on
+    int k1;
+
+    // column: byte offset of this lane's column (4 or 16 of them, in turn), or
+    // kNowhere.
+    __device__ __forceinline__ Sums(const uint8_t* const (&rows)[R], const int (&bytes)[R],
+                                    const uint8_t* columns, uint32_t plane, uint32_t column, int K,
+                                    int end, uint8_t* ring, uint32_t ring0)
+        : lds0(ring0), lds(ring), k1(end)
+    {
+        const int lane = threadIdx.x & (kWave - 1);
 #pragma unroll
         for (int r = 0; r < R; ++r)
+            rw[r] = rsrc_words(rows[r], bytes[r]);
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                sum[r][g] = WT == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[r][g];
+        for (int v = 0; v < X; ++v)
+            rx[v] = rsrc_words(columns + (int64_t)v * plane, (int)plane);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int half = 0; half < 2; ++half) {
+            const int row = half * 8 + (lane >> 3), chunk = (lane & 7) ^ key(row);
+            woff[half] = (uint32_t)row * (uint32_t)K + (uint32_t)chunk * 16u;
+            wleft[half] = K - chunk * 16;
+        }
+        const int c = kPacked ? (lane & 15) >> 2 : 0;
+        const int at = c / 2 * 64 + (lane >> 4) * 16 + c % 2 * 8;
+        xoff = column == kNowhere ? kNowhere : column + (uint32_t)at * 2u;
+        xleft = K - at;
+    }
+
+    // Place of a row's chunk: exclusive-or with this (rows 0 to 15).
+    static __device__ __forceinline__ int key(int row) { return (row >> 1) & 7; }
+
+    // Step k's loads.
+    __device__ __forceinline__ void load(int k, int slot) const
+    {
+        const uint32_t dst = lds0 + slot * kBytes;
+        const int at = k * kBlockK;
+        const bool mine = k < k1;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const u32x4 w = widened8<WT, XT>(s.w[r][c >> 1][(c & 1) * 2],
-                                                 s.w[r][c >> 1][(c & 1) * 2 + 1]);
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t to = mine && at < wleft[half] ? woff[half] : kNowhere;
 #pragma unroll
-                for (int v = 0; v < X; ++v)
-#pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        sum[r][g] = product<XT>(w, s.x[g][v][c], sum[r][g]);
-            }
+            for (int r = 0; r < R; ++r)
+                load_to_lds<true>(rw[r], dst + (2 * r + half) * 1024, to, (uint32_t)at);
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float f = WT == 0 ? scale(r, k) : 0.0f;
+        for (int i = 0; i < kXLoads; ++i) {
+            const int more = i / 2 * 64 + i % 2 * 8;  // elements (packed: 0)
+            const uint32_t to = mine && at + more < xleft ? xoff + more * 2u : kNowhere;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
+            for (int v = 0; v < X; ++v)
+                load_to_lds<false>(rx[v], dst + (2 * R + v * kXLoads + i) * 1024, to,
+                                   (uint32_t)at * 2u);
+        }
+    }
+
+    // scale(r, k): operand r's scale of step k, of FP8 weights.
+    template <class Scale>
+    __device__ __forceinline__ void operator()(int k0, Scale&& scale,
+                                               f32x4 (&acc)[R]) const
+    {
+        const int lane = threadIdx.x & (kWave - 1);
+        const int q = lane >> 4, i16 = lane & 15;
+        const uint32_t wat = (uint32_t)i16 * 128u + (uint32_t)((q ^ key(i16)) * 16);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            load(k0 + d, d);
+        int slot = 0;
+        for (int k = k0; k < k1; ++k) {
+            // taken here, so that no branch comes between the products and their
+            // scaling: behind one, the compiler left out the wait states that a
+            // matrix instruction's result needs (element 3 of each was wrong)
+            float f[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                f[r] = WT == 0 ? scale(r, k) : 1.0f;
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kAll) : "memory");
+            const uint8_t* from = lds + slot * kBytes;
+            u32x4 w[R][2], x[X][kXLoads];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)  // of the step: chunks q, q + 4
+                    w[r][half] = *reinterpret_cast<const u32x4*>(from + r * 2048 +
+                                                                 (wat ^ half * 64));
+#pragma unroll
+            for (int v = 0; v < X; ++v)
+#pragma unroll
+                for (int i = 0; i < kXLoads; ++i)
+                    x[v][i] = *reinterpret_cast<const u32x4*>(
+                        from + (2 * R + v * kXLoads + i) * 1024 + lane * 16);
+            // read before the slot is loaded again
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            load(k + D, slot);
+            __builtin_amdgcn_sched_barrier(0);
+            slot = slot + 1 == D ? 0 : slot + 1;
+
+            f32x4 sum[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                sum[r] = WT == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[r];
+            u32x4 y[X][4];
+#pragma unroll
+            for (int v = 0; v < X; ++v) {
+                if constexpr (kPacked) {
+                    y[v][0] = x[v][0];
+                    y[v][1] = rotated<4>(x[v][0]);
+                    y[v][2] = rotated<8>(x[v][0]);
+                    y[v][3] = rotated<12>(x[v][0]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        y[v][c] = x[v][c % kXLoads];
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const u32x4 o = widened8<WT, XT>(w[r][c >> 1][(c & 1) * 2],
+                                                     w[r][c >> 1][(c & 1) * 2 + 1]);
+#pragma unroll
+                    for (int v = 0; v < X; ++v)
+                        sum[r] = product<XT>(o, y[v][c], sum[r]);
+                }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
                 if constexpr (WT == 0) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[r][g][i] = __builtin_fmaf(f, sum[r][g][i], acc[r][g][i]);
+                        acc[r][i] = __builtin_fmaf(f[r], sum[r][i], acc[r][i]);
                 } else {
-                    acc[r][g] = sum[r][g];
+                    acc[r] = sum[r];
                 }
             }
         }
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-        load(k0 + d, in[d]);
-    for (int k = k0; k < k1; k += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (k + d < k1)
-                use(k + d, in[d]);
-            load(k + d + D, in[d]);
-        }
+        // loads past the end may not write what comes next in LDS; and the last
+        // products' wait states, which the loop's end is a branch before
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     }
-}
+};
 
 // Scales of up to 64 steps from k0 on, one a lane, and one of them.
 struct StepScales {
@@ -272,6 +441,7 @@ struct StepScales {
     {
         const int k = held + (int)(threadIdx.x & (kWave - 1));
         v = k < k1 ? from[k] : 0.0f;
+        asm volatile("" : "+v"(v));  // here already: a wait later is for later loads too
     }
     __device__ __forceinline__ float at(int k)
     {
@@ -283,191 +453,210 @@ struct StepScales {
     }
 };
 
-// Runs f with the number of groups of 16 that hold n columns, at most kMost.
-template <int kMost, class F>
-__device__ __forceinline__ void with_groups(int n, F&& f)
-{
-    if (kMost == 1 || n <= 16)
-        f(std::integral_constant<int, 1>());
-    else if (n <= 32)
-        f(std::integral_constant<int, kMost == 1 ? 1 : 2>());
-    else
-        f(std::integral_constant<int, kMost == 1 ? 1 : 4>());
-}
+// A kind of Sums as a value.
+template <class S>
+struct Kind {
+    using type = S;
+    static constexpr bool kPacked = S::kPacked;
+};
 
-// Gate and up. kMost: 1 for calls of up to 16 tokens, else 4.
-template <int WT, int XT, int kMost>
-__global__ __launch_bounds__(kUpWaves * kWave) __attribute__((amdgpu_waves_per_eu(kMost == 1 ? 4 : 2)))
-void block_few_up_kernel(FewArgs a)
+// Gate and up, of 8 R hidden columns a block.
+template <int WT, int XT, int R, bool kSmall>
+__global__ __launch_bounds__(kUpWaves * kWave) void block_few_up_kernel(FewArgs a)
 {
-    __shared__ Routing s;
-    __shared__ int s_list[kFewMaxTokens];
-    __shared__ int s_n;
-    __shared__ f32x4 s_sum[kUpWaves][2][kMost][kWave];
+    using Few = Sums<R, 4, 1, WT, XT, 2>;    // steps in flight: as fit kRing
+    using More = Sums<R, 16, 1, WT, XT, 1>;
+    constexpr int kRing = 2 * Few::kBytes;
+    static_assert(More::kBytes <= kRing && sizeof(f32x4) * R * kWave <= kRing, "LDS of a wave");
+    constexpr int kCols = 8 * R;
+    __shared__ __align__(1024) uint8_t s_ring[kUpWaves][kRing];
+    static_assert(sizeof s_ring >= kMaxWords * 4, "the routing's scratch");
+    __shared__ int s_list[kUpWaves][kFewMaxTokens];
+    const uint32_t ring0 =
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&s_ring[0][0];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
-    const int tiles = a.I / 16;
+    const int tiles = a.I / kCols;
     const int u = (int)blockIdx.x / tiles, tile = (int)blockIdx.x % tiles;
-    read_routing<kUpWaves * kWave>(a, s);
-    if (u >= s.hits)
-        return;  // the whole block
-    const int e = uniform(s.hit[u]);
-    if (wave == 0) {
-        const int n = slots_of(s, a.T * a.topk, e, s_list);
-        if (lane == 0)
-            s_n = n;
-    }
-    __syncthreads();
-    const int n = uniform(s_n);
-    const int64_t row = (int64_t)e * 2 * a.I + tile * 16;
-    const __amdgpu_buffer_rsrc_t rw[2] = {
-        row_rsrc(a.up + row * a.H, (uint32_t)a.H * 16u),
-        row_rsrc(a.up + (row + a.I) * a.H, (uint32_t)a.H * 16u)};
-    const __amdgpu_buffer_rsrc_t rx[1] = {row_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H * 2u)};
-    const int steps = (a.H + kBlockK - 1) / kBlockK;
-    const int k0 = steps * wave / kUpWaves, k1 = steps * (wave + 1) / kUpWaves;
-
-    with_groups<kMost>(n, [&](auto groups) {
-        constexpr int G = decltype(groups)::value;
-        uint32_t xoff[G];
+    with_routing<kSmall, kUpWaves * kWave>(a, s_ring[0], [&](const auto& routing) {
+        if (u >= routing.hits)
+            return;  // the whole block
+        const int e = routing.expert(u);
+        int* list = s_list[wave];  // every wave has its own
+        const int n = routing.slots_of(a, e, list);
+        // operands: R / 2 of gate rows, then the same of up rows
+        const int64_t row = (int64_t)e * 2 * a.I + tile * kCols;
+        const uint8_t* rows[R];
+        int bytes[R];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int c = g * 16 + (lane & 15);
-            xoff[g] = c < n ? (uint32_t)(s_list[c] / a.topk) * (uint32_t)a.H * 2u : kNowhere;
+        for (int r = 0; r < R; ++r) {
+            rows[r] = a.up + (row + r % (R / 2) * 16 + (r < R / 2 ? 0 : a.I)) * a.H;
+            bytes[r] = a.H * 16;
         }
-        f32x4 acc[2][G];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int steps = (a.H + kBlockK - 1) / kBlockK;
+        const int k0 = steps * wave / kUpWaves, k1 = steps * (wave + 1) / kUpWaves;
         const int blocks = a.H / kBlockK;  // of a row's scales (FP8)
-        const float* first = a.ups + (row / 128) * blocks;
-        StepScales sg(WT == 0 ? first : a.ups, WT == 0 ? k0 : 0, WT == 0 ? k1 : 0);
-        StepScales su(WT == 0 ? first + (int64_t)(a.I / 128) * blocks : a.ups, WT == 0 ? k0 : 0,
-                      WT == 0 ? k1 : 0);
-        accumulate<2, G, 1, WT, XT, G == 1 ? 2 : 1>(
-            rw, rx, xoff, a.H, k0, k1, [&](int r, int k) { return r == 0 ? sg.at(k) : su.at(k); },
-            acc);
+        const float* first = a.ups + (WT == 0 ? (row / 128) * blocks : 0);
+        const float* second = first + (WT == 0 ? (int64_t)(a.I / 128) * blocks : 0);
+        f32x4* mine = reinterpret_cast<f32x4*>(s_ring[wave]);  // its sums, when it is done
+
+        for (int c0 = 0; c0 < n; c0 += 16) {
+            auto sums = [&](auto kind) {
+                using S = decltype(kind);
+                const int c = c0 + (lane & (S::kPacked ? 3 : 15));
+                const uint32_t column =
+                    c < n ? (uint32_t)(list[c] / a.topk) * (uint32_t)a.H * 2u : kNowhere;
+                f32x4 acc[R];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+                for (int r = 0; r < R; ++r)
+                    acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                StepScales sg(first, k0, WT == 0 ? k1 : k0), su(second, k0, WT == 0 ? k1 : k0);
+                typename S::type(rows, bytes, a.x, (uint32_t)a.T * (uint32_t)a.H * 2u, column, a.H,
+                                 k1, s_ring[wave], ring0 + wave * kRing)(
+                    k0, [&](int r, int k) { return r < R / 2 ? sg.at(k) : su.at(k); }, acc);
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                s_sum[wave][r][g][lane] = acc[r][g];
-    });
-    __syncthreads();
-    // wave g finishes group g: a lane has 4 hidden columns of one token
-    if (wave * 16 < n) {
-        const int c = wave * 16 + (lane & 15);
-        f32x4 v[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            v[r] = s_sum[0][r][wave][lane];
-#pragma unroll
-            for (int w = 1; w < kUpWaves; ++w)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[r][i] = v[r][i] + s_sum[w][r][wave][lane][i];
-        }
-        const int col = tile * 16 + (lane >> 4) * 4;
-        if (c < n) {
-            float z[4], rest[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float g = v[0][i], up = v[1][i];
-                if constexpr (WT == 1) {
-                    const int64_t at = (int64_t)e * 2 * a.I + col + i;
-                    g = g * a.ups[at];
-                    up = up * a.ups[at + a.I];
-                }
-                const float y = silu_times(g, up);
-                z[i] = round_to<0>(y);
-                rest[i] = z[i] == y ? 0.0f : y - z[i];  // (an infinity has no rest)
-            }
-            const int64_t at = (int64_t)s_list[c] * a.I + col;
-            const int64_t plane = (int64_t)a.T * a.topk * a.I;
-            auto pair = [](float lo, float hi) {
-                return (__builtin_bit_cast(uint32_t, round_to<0>(lo)) >> 16) |
-                       (__builtin_bit_cast(uint32_t, round_to<0>(hi)) & 0xFFFF0000u);
+                for (int r = 0; r < R; ++r)
+                    mine[r * kWave + lane] = acc[r];
             };
-            *reinterpret_cast<u32x2*>(a.act + at * 2) = u32x2{pair(z[0], z[1]), pair(z[2], z[3])};
-            *reinterpret_cast<u32x2*>(a.act + (plane + at) * 2) =
-                u32x2{pair(rest[0], rest[1]), pair(rest[2], rest[3])};
+            if (n <= 4)
+                sums(Kind<Few>());
+            else
+                sums(Kind<More>());
+            __syncthreads();
+            // a lane has 4 hidden columns of one token; wave r those of gate
+            // operand r
+            const int c = c0 + (lane & 15);
+            if (wave < R / 2 && c < n) {
+                f32x4 v[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at = (wave + h * (R / 2)) * kWave + lane;
+                    v[h] = reinterpret_cast<const f32x4*>(s_ring[0])[at];
+#pragma unroll
+                    for (int w = 1; w < kUpWaves; ++w) {
+                        const f32x4 o = reinterpret_cast<const f32x4*>(s_ring[w])[at];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[h][i] = v[h][i] + o[i];
+                    }
+                }
+                const int col = tile * kCols + wave * 16 + (lane >> 4) * 4;
+                float z[4], rest[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float g = v[0][i], up = v[1][i];
+                    if constexpr (WT == 1) {
+                        const int64_t at = (int64_t)e * 2 * a.I + col + i;
+                        g = g * a.ups[at];
+                        up = up * a.ups[at + a.I];
+                    }
+                    const float y = silu_times(g, up);
+                    z[i] = round_to<0>(y);
+                    rest[i] = z[i] == y ? 0.0f : y - z[i];  // (an infinity has no rest)
+                }
+                const int64_t at = (int64_t)list[c] * a.I + col;
+                const int64_t plane = (int64_t)a.T * a.topk * a.I;
+                auto pair = [](float lo, float hi) {
+                    return (__builtin_bit_cast(uint32_t, round_to<0>(lo)) >> 16) |
+                           (__builtin_bit_cast(uint32_t, round_to<0>(hi)) & 0xFFFF0000u);
+                };
+                *reinterpret_cast<u32x2*>(a.act + at * 2) =
+                    u32x2{pair(z[0], z[1]), pair(z[2], z[3])};
+                *reinterpret_cast<u32x2*>(a.act + (plane + at) * 2) =
+                    u32x2{pair(rest[0], rest[1]), pair(rest[2], rest[3])};
+            }
+            if (c0 + 16 < n)
+                __syncthreads();  // the sums have been read
         }
-    }
+    });
 }
 
-// Down and the sum over experts, of 16 R output columns.
-template <int WT, int XT, int R, int kMost>
-__global__ __launch_bounds__(kDownWaves * kWave) __attribute__((amdgpu_waves_per_eu(kMost == 1 ? 4 : 2)))
-void block_few_down_kernel(FewArgs a)
+// Down and the sum over experts, of 16 R output columns a block. D: steps of
+// up to 4 columns in flight.
+template <int WT, int XT, int R, int D, bool kSmall>
+__global__ __launch_bounds__(kDownWaves * kWave) void block_few_down_kernel(FewArgs a)
 {
-    extern __shared__ float s_y[];  // [splits][T * topk][16 R]
-    __shared__ Routing s;
+    using Few = Sums<R, 4, 2, WT, 0, D>;
+    using More = Sums<R, 16, 2, WT, 0, 1>;
+    constexpr int kRing = D * Few::kBytes > More::kBytes ? D * Few::kBytes : More::kBytes;
+    extern __shared__ __align__(1024) uint8_t s_mem[];  // rings, [splits][T * topk][16 R] sums
     __shared__ int s_list[kDownWaves][kFewMaxTokens];
+    __shared__ int s_id[kSmall ? kWave : 1];
+    const int* id = s_id;  // the experts of the slots that are their token's first of it
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
+    uint8_t* ring = s_mem + wave * kRing;
+    const uint32_t ring0 =
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring;
+    float* s_y = reinterpret_cast<float*>(s_mem + kDownWaves * kRing);
     constexpr int kCols = 16 * R;
     const int h0 = (int)blockIdx.x * kCols;
     const int P = a.T * a.topk;
-    read_routing<kDownWaves * kWave>(a, s);
-    const uint32_t plane = (uint32_t)P * (uint32_t)a.I * 2u;
-    const __amdgpu_buffer_rsrc_t rx[2] = {row_rsrc(a.act, plane), row_rsrc(a.act + plane, plane)};
-    const int steps = (a.I + kBlockK - 1) / kBlockK;
-    const int items = uniform(s.hits) * a.splits;
-    for (int item = wave; item < items; item += kDownWaves) {
-        const int e = uniform(s.hit[item / a.splits]), split = item % a.splits;
-        const int n = slots_of(s, P, e, s_list[wave]);
-        const int k0 = steps * split / a.splits, k1 = steps * (split + 1) / a.splits;
-        const int64_t row = (int64_t)e * a.H + h0;
-        __amdgpu_buffer_rsrc_t rw[R];
+    with_routing<kSmall, kDownWaves * kWave>(a, s_mem, [&](const auto& routing) {
+        if constexpr (kSmall) {
+            if (wave == 0)
+                s_id[lane] = routing.id;
+        } else {
+            id = routing.s.id;
+        }
+        const int steps = (a.I + kBlockK - 1) / kBlockK;
+        const int items = routing.hits * a.splits;
+        int* list = s_list[wave];
+        for (int item = wave; item < items; item += kDownWaves) {
+            const int e = routing.expert(item / a.splits), split = item % a.splits;
+            const int n = routing.slots_of(a, e, list);
+            const int k0 = uniform(steps * split / a.splits);
+            const int k1 = uniform(steps * (split + 1) / a.splits);
+            const int64_t row = (int64_t)e * a.H + h0;
+            const uint8_t* rows[R];
+            int bytes[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r)  // (H may end inside the block)
-            rw[r] = row_rsrc(a.down + (row + r * 16) * a.I,
-                             h0 + r * 16 < a.H ? (uint32_t)a.I * 16u : 0u);
-        with_groups<kMost>(n, [&](auto groups) {
-            constexpr int G = decltype(groups)::value;
-            uint32_t xoff[G];
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int c = g * 16 + (lane & 15);
-                xoff[g] = c < n ? (uint32_t)s_list[wave][c] * (uint32_t)a.I * 2u : kNowhere;
+            for (int r = 0; r < R; ++r) {  // (H may end inside the block)
+                rows[r] = a.down + (row + r * 16) * a.I;
+                bytes[r] = h0 + r * 16 < a.H ? a.I * 16 : 0;
             }
-            f32x4 acc[R][G];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-                    acc[r][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             // (a block's columns lie in one block of 128)
-            StepScales sc(WT == 0 ? a.downs + (row / 128) * (a.I / kBlockK) : a.downs,
-                          WT == 0 ? k0 : 0, WT == 0 ? k1 : 0);
-            accumulate<R, G, 2, WT, 0, G == 1 ? 2 : 1>(
-                rw, rx, xoff, a.I, k0, k1, [&](int, int k) { return sc.at(k); }, acc);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int c = g * 16 + (lane & 15);
-                if (c < n) {
-                    float* y = s_y + ((int64_t)split * P + s_list[wave][c]) * kCols + (lane >> 4) * 4;
+            const float* first = a.downs + (WT == 0 ? (row / 128) * (a.I / kBlockK) : 0);
+            for (int c0 = 0; c0 < n; c0 += 16) {
+                auto sums = [&](auto kind) {
+                    using S = decltype(kind);
+                    const int cx = c0 + (lane & (S::kPacked ? 3 : 15));
+                    const uint32_t column = cx < n ? (uint32_t)list[cx] * (uint32_t)a.I * 2u : kNowhere;
+                    f32x4 acc[R];
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        *reinterpret_cast<f32x4*>(y + r * 16) = acc[r][g];
-                }
+                        acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    StepScales sc(first, k0, WT == 0 ? k1 : k0);
+                    typename S::type(rows, bytes, a.act, (uint32_t)P * (uint32_t)a.I * 2u, column,
+                                     a.I, k1, ring, ring0)(
+                        k0, [&](int, int k) { return sc.at(k); }, acc);
+                    const int c = c0 + (lane & 15);
+                    if (c < n) {
+                        float* y = s_y + (split * P + list[c]) * kCols + (lane >> 4) * 4;
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            *reinterpret_cast<f32x4*>(y + r * 16) = acc[r];
+                    }
+                };
+                if (n <= 4)
+                    sums(Kind<Few>());
+                else
+                    sums(Kind<More>());
             }
-        });
-    }
+        }
+    });
     __syncthreads();
     // a token's pairs in slot order, each the sum of its pieces in order
     for (int i = threadIdx.x; i < a.T * kCols; i += kDownWaves * kWave) {
         const int t = i / kCols, c = i % kCols;
         float sum = 0.0f;
         for (int j = 0; j < a.topk; ++j) {
-            const int p = t * a.topk + j, e = s.id[p];
+            const int p = t * a.topk + j, e = id[p];
             if (e < 0 || h0 + c >= a.H)
                 continue;
-            float y = s_y[(int64_t)p * kCols + c];
+            float y = s_y[p * kCols + c];
             for (int k = 1; k < a.splits; ++k)
-                y = y + s_y[((int64_t)k * P + p) * kCols + c];
+                y = y + s_y[(k * P + p) * kCols + c];
             if constexpr (WT == 1)
                 y = y * a.downs[(int64_t)e * a.H + h0 + c];
             float weight = 1.0f;
@@ -490,27 +679,48 @@ void block_few_down_kernel(FewArgs a)
     }
 }
 
-template <int WT, int XT, int kMost>
+// (hipErrorInvalidValue for more LDS than a compute unit has)
+template <int WT, int XT, int R, int D, bool kSmall>
+hipError_t launch_down(const FewArgs& a, hipStream_t s)
+{
+    constexpr int kFew = Sums<R, 4, 2, WT, 0, D>::kBytes * D, kMore = Sums<R, 16, 2, WT, 0, 1>::kBytes;
+    const size_t lds = (size_t)kDownWaves * (kFew > kMore ? kFew : kMore) +
+                       (size_t)a.splits * a.T * a.topk * 16 * R * sizeof(float);
+    constexpr size_t kStatic = (kSmall ? kWave * sizeof(int) : sizeof(Routing) + sizeof(int)) +
+                               kDownWaves * kFewMaxTokens * sizeof(int);
+    if (lds + (kStatic + 1023) / 1024 * 1024 > kFewLds)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((block_few_down_kernel<WT, XT, R, D, kSmall>),
+                       dim3((a.H + 16 * R - 1) / (16 * R)), dim3(kDownWaves * kWave), lds, s, a);
+    return hipGetLastError();
+}
+
+template <int WT, int XT, bool kSmall>
 hipError_t few_with(const FewArgs& a, hipStream_t s)
 {
-    const dim3 up((unsigned)(a.hits * (a.I / 16)));
-    hipLaunchKernelGGL((block_few_up_kernel<WT, XT, kMost>), up, dim3(kUpWaves * kWave), 0, s, a);
-    const size_t pair = (size_t)a.splits * a.T * a.topk * sizeof(float);
-    // 32 columns a block where that leaves half the compute units a block and
-    // the pairs' sums fit
-    if (a.H >= 32 * 128 && pair * 32 <= 96 * 1024)
-        hipLaunchKernelGGL((block_few_down_kernel<WT, XT, 2, kMost>), dim3((a.H + 31) / 32),
-                           dim3(kDownWaves * kWave), pair * 32, s, a);
+    // 32 hidden columns a block where they fill the compute units twice
+    const int up = a.hits * (a.I / 16);
+    if (a.I % 32 == 0 && up >= 1024)
+        hipLaunchKernelGGL((block_few_up_kernel<WT, XT, 4, kSmall>), dim3(up / 2),
+                           dim3(kUpWaves * kWave), 0, s, a);
     else
-        hipLaunchKernelGGL((block_few_down_kernel<WT, XT, 1, kMost>), dim3(a.H / 16),
-                           dim3(kDownWaves * kWave), pair * 16, s, a);
-    return hipGetLastError();
+        hipLaunchKernelGGL((block_few_up_kernel<WT, XT, 2, kSmall>), dim3(up), dim3(kUpWaves * kWave),
+                           0, s, a);
+    // 32 output columns a block where that leaves most compute units a block and
+    // the pairs' sums leave LDS for three steps; else 16, with two steps of the
+    // largest calls
+    const int pairs = a.splits * a.T * a.topk;
+    if (kSmall && a.H >= 32 * 192 && pairs <= 64)
+        return launch_down<WT, XT, 2, 3, kSmall>(a, s);
+    if (pairs <= 832)
+        return launch_down<WT, XT, 1, 3, kSmall>(a, s);
+    return launch_down<WT, XT, 1, 2, kSmall>(a, s);
 }
 
 template <int WT, int XT>
 hipError_t few_types(const FewArgs& a, hipStream_t s)
 {
-    return a.T <= 16 ? few_with<WT, XT, 1>(a, s) : few_with<WT, XT, 4>(a, s);
+    return a.T * a.topk <= kWave ? few_with<WT, XT, true>(a, s) : few_with<WT, XT, false>(a, s);
 }
 
 }  // namespace
