@@ -47,7 +47,7 @@ __global__ __launch_bounds__(W * kWave) void block_norm_backward_kernel(NormBack
     constexpr bool kAhead = C <= 2;
     // longer rows leave no registers for their values: read again for the second pass
     constexpr bool kAgain = !kAhead;
-    __shared__ float s_sum[2][kSums][W];
+    __shared__ float s_sum[2][kSums][W];  // (those of waves that are not there stay 0)
     const int lane = threadIdx.x & (kWave - 1);
     const int part = uniform(threadIdx.x / kWave);
     const int waves = a.row_waves;
@@ -126,19 +126,42 @@ __global__ __launch_bounds__(W * kWave) void block_norm_backward_kernel(NormBack
         for (int c = 0; c < C; ++c)
             load_chunk(row, c, x);
     };
-    auto weight = [&](const uint8_t* w, bool there, int c, float (&f)[8]) {
-        if (there) {
-            int e = e0 + c * kNormChunk;
-            if (C > 2)  // loaded in each pass, not kept between them
-                asm volatile("" : "+v"(e));
-            weights8<WT>(row_rsrc(w, wbytes), e, f);
-        } else {
+    // The weights of this lane's columns: held over the rows where there are
+    // registers, as a load of them between two rows would be waited for with
+    // all of the next row's before it; else loaded in each pass.
+    Weights8<WT> held_post[kAhead ? C : 1], held_gate[kAhead ? C : 1], held_pre[kAhead ? C : 1];
+    auto hold = [&](const uint8_t* w, bool there, Weights8<WT> (&held)[kAhead ? C : 1]) {
+        const __amdgpu_buffer_rsrc_t rw = row_rsrc(w, there ? wbytes : 0u);
+#pragma unroll
+        for (int c = 0; c < (kAhead ? C : 1); ++c)
+            held[c].load(rw, e0 + c * kNormChunk);
+    };
+    auto weight = [&](const uint8_t* w, bool there, const Weights8<WT> (&held)[kAhead ? C : 1],
+                      int c, float (&f)[8]) {
+        if (!there) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 f[i] = 1.0f;
+        } else if (kAhead) {
+            held[c < (kAhead ? C : 1) ? c : 0].widen8(f);
+        } else {
+            int e = e0 + c * kNormChunk;
+            asm volatile("" : "+v"(e));  // (not kept from one pass to the other)
+            weights8<WT>(row_rsrc(w, wbytes), e, f);
         }
     };
+    if (kAhead) {
+        hold(a.post, has_post, held_post);
+        hold(a.gate, has_gate && a.gates == 1, held_gate);
+        hold(a.pre, has_out, held_pre);
+    }
+    if (threadIdx.x < 2 * kSums * W)
+        (&s_sum[0][0][0])[threadIdx.x] = 0.0f;
+    if (waves > 1)
+        __syncthreads();
+    static_assert(2 * kSums * W <= 3 * kWave, "cleared by 3 waves");
 
+    int64_t gate_group = -1;  // whose gate is held
     int64_t open = g0;  // groups before it have their gate's gradient written
     int parity = 0;
     Raw<C> x;
@@ -148,6 +171,11 @@ __global__ __launch_bounds__(W * kWave) void block_norm_backward_kernel(NormBack
         const int64_t group = g, row = g * a.group_rows + r;
         r += a.group_blocks;
         settle();
+        const uint8_t* gate = has_gate ? a.gate + (a.gates > 1 ? group : 0) * wbytes : nullptr;
+        if (kAhead && has_gate && a.gates > 1 && gate_group != group) {
+            hold(gate, true, held_gate);
+            gate_group = group;
+        }
         Raw<C> next;
         if (kAhead && g < g1)
             load(g * a.group_rows + r, next);
@@ -155,7 +183,6 @@ __global__ __launch_bounds__(W * kWave) void block_norm_backward_kernel(NormBack
             for (; open < group; ++open)
                 close_gate(open);
         }
-        const uint8_t* gate = has_gate ? a.gate + (a.gates > 1 ? group : 0) * wbytes : nullptr;
 
         float s[kSums] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -169,9 +196,9 @@ __global__ __launch_bounds__(W * kWave) void block_norm_backward_kernel(NormBack
             widen<DT>(x.h[c], h);
             widen<DT>(x.gh[c], gh);
             widen<DT>(x.go[c], go);
-            weight(a.post, has_post, c, wp);
-            weight(gate, has_gate, c, wg);
-            weight(a.pre, has_out, c, w2);
+            weight(a.post, has_post, held_post, c, wp);
+            weight(gate, has_gate, held_gate, c, wg);
+            weight(a.pre, has_out, held_pre, c, w2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float q = wg[i] * wp[i] * y[i], d2 = go[i] * w2[i];
@@ -193,11 +220,21 @@ __global__ __launch_bounds__(W * kWave) void block_norm_backward_kernel(NormBack
                     s_sum[parity][k][part] = s[k];
             }
             __syncthreads();
+            // a lane a wave and sum: one read, and a tree over the waves
+            static_assert(W == 8 || W == 16, "lanes of a sum");
+            constexpr int kEach = kWave / W;  // sums a read
 #pragma unroll
-            for (int k = 0; k < kSums; ++k) {
-                s[k] = s_sum[parity][k][0];
-                for (int w = 1; w < waves; ++w)
-                    s[k] = s[k] + s_sum[parity][k][w];
+            for (int k0 = 0; k0 < kSums; k0 += kEach) {
+                const int at = k0 * W + lane;
+                float v = (&s_sum[parity][0][0])[at < kSums * W ? at : 0];
+                v = v + dpp<kDppXor1>(v);
+                v = v + dpp<kDppXor2>(v);
+                v = v + dpp<kDppHalfMirror>(v);
+                if (W == 16)
+                    v = v + dpp<kDppMirror>(v);
+#pragma unroll
+                for (int k = k0; k < kSums && k < k0 + kEach; ++k)
+                    s[k] = lane_value(v, (k - k0) * W);
             }
             parity ^= 1;  // the next row's sums go where no wave reads any more
         }
@@ -226,9 +263,9 @@ __global__ __launch_bounds__(W * kWave) void block_norm_backward_kernel(NormBack
             widen<DT>(x.h[c], h);
             widen<DT>(x.gh[c], gh);
             widen<DT>(x.go[c], go);
-            weight(a.post, has_post, c, wp);
-            weight(gate, has_gate, c, wg);
-            weight(a.pre, has_out, c, w2);
+            weight(a.post, has_post, held_post, c, wp);
+            weight(gate, has_gate, held_gate, c, wg);
+            weight(a.pre, has_out, held_pre, c, w2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float n2 = h[i] * r2;

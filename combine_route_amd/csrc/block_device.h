@@ -82,22 +82,40 @@ __device__ __forceinline__ float silu_times(float g, float u)
     return g * 0.0625f * __builtin_amdgcn_rcpf(d) * u;
 }
 
-// 8 weights from element e on. WT: 0 bf16, 1 fp16, 2 fp32.
+// 8 weights as they lie. WT: 0 bf16, 1 fp16, 2 fp32.
+template <int WT>
+struct Weights8 {
+    static constexpr int kBytes = WT == 2 ? 4 : 2;
+    u32x4 v[WT == 2 ? 2 : 1];
+
+    // From element e on; zeros past the resource.
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int e)
+    {
+#pragma unroll
+        for (int i = 0; i < (WT == 2 ? 2 : 1); ++i)
+            v[i] = bload16<0>(r, (uint32_t)e * kBytes + 16u * i);
+    }
+
+    __device__ __forceinline__ void widen8(float (&w)[8]) const
+    {
+        if constexpr (WT == 2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u = v[i / 4][i % 4];  // bit_cast reads a vector's element 0
+                w[i] = __builtin_bit_cast(float, u);
+            }
+        } else {
+            widen<WT>(v[0], w);
+        }
+    }
+};
+
 template <int WT>
 __device__ __forceinline__ void weights8(__amdgpu_buffer_rsrc_t r, int e, float (&w)[8])
 {
-    if constexpr (WT == 2) {
-        const u32x4 lo = bload16<0>(r, (uint32_t)e * 4u);
-        const u32x4 hi = bload16<0>(r, (uint32_t)e * 4u + 16u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t l = lo[i], u = hi[i];  // bit_cast reads a vector's element 0
-            w[i] = __builtin_bit_cast(float, l);
-            w[4 + i] = __builtin_bit_cast(float, u);
-        }
-    } else {
-        widen<WT>(bload16<0>(r, (uint32_t)e * 2u), w);
-    }
+    Weights8<WT> v;
+    v.load(r, e);
+    v.widen8(w);
 }
 
 }  // namespace dev

@@ -11,8 +11,8 @@
 //
 // Each mean of squares is summed the same way whatever the number of waves:
 // FP32 sums of chunks of 512 elements (8 elements a lane in order, then a
-// fixed tree over the lanes), added in chunk order. A row's result therefore
-// does not depend on the other rows of the call.
+// fixed tree over the lanes), added by a fixed tree over the chunks. A row's
+// result therefore does not depend on the other rows of the call.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,37 +26,39 @@ namespace {
 using namespace block::dev;
 
 // Sum of squares of a row, the waves that share it adding their chunks'
-// sums in order through s (an array of this sum's own).
+// sums through s (an array of this sum's own).
 template <int C>
-__device__ __forceinline__ float square_sum(const float (&v)[C][8], float* s, int part,
+__device__ __forceinline__ float square_sum(const float (&h)[C][8], float* s, int part,
                                             int row_waves, int lane)
 {
     float sums[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        float q = v[c][0] * v[c][0];
+        float q = h[c][0] * h[c][0];
 #pragma unroll
         for (int i = 1; i < 8; ++i)
-            q = __builtin_fmaf(v[c][i], v[c][i], q);
+            q = __builtin_fmaf(h[c][i], h[c][i], q);
         sums[c] = wave_sum(q);
     }
-    // chunks past the row are zeros and change nothing
-    float total = 0.0f;
+    // the chunks' sums by a fixed tree over 64 of them; those past the row are
+    // zeros and change nothing
     if (row_waves == 1) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            total = total + sums[c];
-        return total;
+        if constexpr (C == 1)
+            return sums[0];
+        else if constexpr (C == 2)
+            return sums[0] + sums[1];
+        else
+            return (sums[0] + sums[1]) + (sums[2] + sums[3]);
     }
+    static_assert(kNormMaxWaves * C <= kWave && C <= 4, "a lane a chunk");
     if (lane == 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
             s[part * C + c] = sums[c];
     }
     __syncthreads();
-    for (int i = 0; i < row_waves * C; ++i)
-        total = total + s[i];
-    return total;
+    const float v = s[lane < row_waves * C ? lane : 0];
+    return wave_sum(lane < row_waves * C ? v : 0.0f);
 }
 
 __device__ __forceinline__ float inverse_rms(float total, int H, float eps)
@@ -199,8 +201,7 @@ __global__ __launch_bounds__(kNormMaxWaves * kWave) void block_norm_kernel(NormA
         if (lane == 0)
             s[part] = top;
         __syncthreads();
-        for (int i = 0; i < a.row_waves; ++i)
-            top = top > s[i] ? top : s[i];
+        top = wave_umax(s[lane < a.row_waves ? lane : 0]);
     }
     float s, f;
     int8_scale(top, &s, &f);

@@ -62,8 +62,7 @@ __global__ __launch_bounds__(kQuantMaxWaves * kWave) void block_quantize_kernel(
         if (lane == 0)
             s[part] = top;
         __syncthreads();
-        for (int i = 0; i < a.row_waves; ++i)
-            top = top > s[i] ? top : s[i];
+        top = wave_umax(s[lane < a.row_waves ? lane : 0]);
     }
     float s, f;
     int8_scale(top, &s, &f);
