@@ -161,11 +161,12 @@ def _weights(weights, shape, H, rows, x_dtype, dtype, index):
     """Addresses of the post weight, gate and pre weight, rows a gate, and the
     weights' type, which they share."""
     post, gate, pre = weights
-    wt = next((w.dtype for w in weights if isinstance(w, torch.Tensor)), x_dtype)
-    if wt != x_dtype and wt != torch.float32:
+    some = post if post is not None else gate if gate is not None else pre
+    wt = x_dtype if some is None else getattr(some, "dtype", x_dtype)
+    if wt is not x_dtype and wt is not torch.float32:
         raise ValueError(f"weights must be {x_dtype} or torch.float32, not {wt}")
     gate_rows, gate_shape = 0, (H,)
-    if isinstance(gate, torch.Tensor) and gate.dim() != 1:
+    if gate is not None and isinstance(gate, torch.Tensor) and gate.dim() != 1:
         if len(shape) < 2 or shape[0] == 0:
             raise ValueError("a gate [G, H] needs rows of shape [G, ..., H] with G >= 1")
         gate_shape, gate_rows = (shape[0], H), rows // shape[0]
