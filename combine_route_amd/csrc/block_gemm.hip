@@ -208,10 +208,11 @@ struct Operands {
 // half multiplies while the second half's operands are read; then a barrier
 // says that every wave has them, so that the step's place is free for the
 // slice `stages` further, and that the next step's slice is there, from which
-// the second half reads.
+// the second half reads. fresh: no immediate stores came after the first
+// slices' loads, so that none may be allowed for in the waits.
 template <int TS, bool kSwiglu>
 __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uint8_t* lds, int nk,
-                                         const Stores<TS, kSwiglu>& stores,
+                                         const Stores<TS, kSwiglu>& stores, bool fresh,
                                          i32x16 (&acc)[TS][kSubs])
 {
     using L = Loads<TS, kSwiglu>;
@@ -265,7 +266,10 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
             fetch(half, i, stage);
     };
 
-    phase_end<(S - 1) * L::kAll + St::kNow>();
+    if (fresh)
+        phase_end<(S - 1) * L::kAll>();
+    else
+        phase_end<(S - 1) * L::kAll + St::kNow>();
 #pragma unroll
     for (int i = 0; i < kFetches; ++i)
         fetch(0, i, 0);
@@ -292,7 +296,10 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld, const uin
             for (int i = p * kEach / kProducts; i < (p + 1) * kEach / kProducts; ++i)
                 stores.later(D * St::kEach + i);
         });
-        phase_end<(S - 2) * L::kAll + kEach + kBefore + kFirst>();
+        if (kFirst > 0 && fresh)
+            phase_end<(S - 2) * L::kAll + kEach + kBefore>();
+        else
+            phase_end<(S - 2) * L::kAll + kEach + kBefore + kFirst>();
         products(1, [&](int p) {
             fetches(p, 0, next);
 #pragma unroll
@@ -498,14 +505,16 @@ block_gemm_kernel(GemmArgs a)
         // loads past the end of a tile of another class may still write
         phase_end<0>();
         Loads<TS, kSwiglu>(a, t, lds0).prologue(slot);
-        bool more = true;
+        bool more = true, fresh = true;
         while (more) {
             t0 += gridDim.x;
             const int64_t next = tile_at(t0);
             if (next >= 0)
                 look_up(next, s_tile[slot ^ 1]);  // read after the steps' barriers
             i32x16 acc[TS][kSubs];
-            multiply<TS, kSwiglu>(Loads<TS, kSwiglu>(a, t, lds0), lds, nk, stores, acc);
+            multiply<TS, kSwiglu>(Loads<TS, kSwiglu>(a, t, lds0), lds, nk, stores, fresh,
+                                  acc);
+            fresh = false;
             const Tile done = t;
             const uint8_t* scales = lds + kScales + slot * kScaleBytes;
             slot ^= 1;

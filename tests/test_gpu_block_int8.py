@@ -137,6 +137,34 @@ def test_without_counts_many_groups_and_tiles():
     check_rows(case, run_rows(case, n, FP16), n)
 
 
+@pytest.mark.parametrize("G,cap,n,k,rows", [
+    (8, 1100, 7168, 2048, [1100, 1000, 300, 64, 1024, 600, 700, 900]),
+    (6, 800, 7168, 1024, [200, 190, 800, 130, 256, 769]),
+    (64, 130, 7168, 1024, [(29 * g) % 131 for g in range(64)]),
+    (8, 1100, 2048, 7168, [1024, 1100, 0, 300, 192, 512, 256, 700])])
+def test_many_tiles_of_new_inputs(G, cap, n, k, rows):
+    """Several tiles a block, of one class after another, over inputs that lie in
+    no cache: the first slices of a tile take their time."""
+    for seed in range(3):
+        case = product_case(G, cap, n, k, 100 + seed)
+        torch.empty(300_000_000, dtype=torch.uint8, device="cuda").fill_(seed)  # out of the caches
+        check_rows(case, run_rows(case, rows, BF16), rows)
+
+
+@pytest.mark.parametrize("rows", [[1100, 1000, 300, 64], [1024, 200, 700, 129]])
+def test_many_tiles_of_gate_and_up(rows):
+    for seed in range(3):
+        case = product_case(4, 1100, 4096, 7168, 200 + seed)
+        case = (case[0], case[1] * 8 / 7168 ** 0.5, case[2], case[3])
+        torch.empty(300_000_000, dtype=torch.uint8, device="cuda").fill_(seed)
+        out = torch.full((4, 1100, 2048), 77.0, dtype=BF16, device="cuda")
+        cra.moe_grouped_gemm_int8_swiglu(*case, out, counts=counts_of(rows))
+        for g in range(4):
+            z, err = swiglu_reference(case, rows[g], g)
+            close_to(out[g, :rows[g]], z, BF16, 0.0, err)
+            assert bool((out[g, rows[g]:] == 77).all())
+
+
 def test_largest_sums_are_exact():
     """The longest k with the largest codes: 2^30 a sum, odd ones among them."""
     a = torch.full((1, 4, 65536), -128, dtype=torch.int8, device="cuda")
