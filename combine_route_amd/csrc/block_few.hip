@@ -22,6 +22,7 @@
 // both sides take k in the same permuted order. FP8 weights: the sum of each
 // 128 elements of k is scaled as it joins the FP32 sum.
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -231,15 +232,16 @@ struct BlockRouting {
 };
 
 // Calls f with the routing, known to every wave: of up to 64 slots (kSmall)
-// without a barrier. scratch: kMaxWords words of LDS that f may use again.
+// without a barrier. routing, bits: LDS for it, the latter (kMaxWords words)
+// only until f is called.
 template <bool kSmall, int N, class F>
-__device__ __forceinline__ void with_routing(const FewArgs& a, uint8_t* scratch, F&& f)
+__device__ __forceinline__ void with_routing(const FewArgs& a, void* routing, void* bits, F&& f)
 {
     if constexpr (kSmall) {
         f(WaveRouting(a));
     } else {
-        __shared__ Routing s;
-        read_routing<N>(a, s, reinterpret_cast<uint32_t*>(scratch));
+        Routing& s = *static_cast<Routing*>(routing);
+        read_routing<N>(a, s, static_cast<uint32_t*>(bits));
         f(BlockRouting{s, uniform(s.hits)});
     }
 }
@@ -267,15 +269,19 @@ __device__ __forceinline__ u32x4 rotated(const u32x4& v)
 // Up to 4 columns lie packed: lane 4 c + i of each 16 has what column i
 // multiplies with the step's operand c, one load a step instead of four, and a
 // rotation of the 16 lanes by 4 c puts it in place (columns 4 and up hold what
-// nobody reads).
+// nobody reads). Up to 2 columns of two planes share the load: lane 4 c + 2 v
+// + i has plane v's.
 template <int R, int C, int X, int WT, int XT, int D>
 struct Sums {
     static constexpr bool kPacked = C <= 4;
+    static constexpr bool kShared = C <= 2 && X == 2;
+    static constexpr int kColumns = kShared ? 2 : kPacked ? 4 : 16;  // in turn over the lanes
+    static constexpr int kPlanes = kShared ? 1 : X;  // loaded apart
     static constexpr int kXLoads = kPacked ? 1 : 4;  // a step and plane of columns
-    static constexpr int kAll = 2 * R + X * kXLoads;
+    static constexpr int kAll = 2 * R + kPlanes * kXLoads;
     static constexpr int kBytes = kAll * 1024;       // a step's
 
-    u32x4 rw[R], rx[X];  // resources: 16 rows of K bytes each; the planes of the columns
+    u32x4 rw[R], rx[kPlanes];  // resources: 16 rows of K bytes each; the planes of the columns
     uint32_t lds0;       // of the ring
     const uint8_t* lds;
     uint32_t woff[2];    // this lane's chunk of the first step, in either 8 rows
@@ -283,7 +289,7 @@ struct Sums {
     int wleft[2], xleft; // elements of k from there on
     int k1;
 
-    // column: byte offset of this lane's column (4 or 16 of them, in turn), or
+    // column: byte offset of this lane's column (kColumns of them, in turn), or
     // kNowhere.
     __device__ __forceinline__ Sums(const uint8_t* const (&rows)[R], const int (&bytes)[R],
                                     const uint8_t* columns, uint32_t plane, uint32_t column, int K,
@@ -295,8 +301,8 @@ struct Sums {
         for (int r = 0; r < R; ++r)
             rw[r] = rsrc_words(rows[r], bytes[r]);
 #pragma unroll
-        for (int v = 0; v < X; ++v)
-            rx[v] = rsrc_words(columns + (int64_t)v * plane, (int)plane);
+        for (int v = 0; v < kPlanes; ++v)
+            rx[v] = rsrc_words(columns + (int64_t)v * plane, (int)(plane * (X / kPlanes)));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int row = half * 8 + (lane >> 3), chunk = (lane & 7) ^ key(row);
@@ -305,7 +311,8 @@ struct Sums {
         }
         const int c = kPacked ? (lane & 15) >> 2 : 0;
         const int at = c / 2 * 64 + (lane >> 4) * 16 + c % 2 * 8;
-        xoff = column == kNowhere ? kNowhere : column + (uint32_t)at * 2u;
+        const uint32_t second = kShared && (lane & 2) ? plane : 0u;
+        xoff = column == kNowhere ? kNowhere : column + second + (uint32_t)at * 2u;
         xleft = K - at;
     }
 
@@ -330,7 +337,7 @@ struct Sums {
             const int more = i / 2 * 64 + i % 2 * 8;  // elements (packed: 0)
             const uint32_t to = mine && at + more < xleft ? xoff + more * 2u : kNowhere;
 #pragma unroll
-            for (int v = 0; v < X; ++v)
+            for (int v = 0; v < kPlanes; ++v)
                 load_to_lds<false>(rx[v], dst + (2 * R + v * kXLoads + i) * 1024, to,
                                    (uint32_t)at * 2u);
         }
@@ -358,7 +365,7 @@ struct Sums {
                 f[r] = WT == 0 ? scale(r, k) : 1.0f;
             asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kAll) : "memory");
             const uint8_t* from = lds + slot * kBytes;
-            u32x4 w[R][2], x[X][kXLoads];
+            u32x4 w[R][2], x[kPlanes][kXLoads];
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -366,7 +373,7 @@ struct Sums {
                     w[r][half] = *reinterpret_cast<const u32x4*>(from + r * 2048 +
                                                                  (wat ^ half * 64));
 #pragma unroll
-            for (int v = 0; v < X; ++v)
+            for (int v = 0; v < kPlanes; ++v)
 #pragma unroll
                 for (int i = 0; i < kXLoads; ++i)
                     x[v][i] = *reinterpret_cast<const u32x4*>(
@@ -387,14 +394,15 @@ struct Sums {
 #pragma unroll
             for (int v = 0; v < X; ++v) {
                 if constexpr (kPacked) {
-                    y[v][0] = x[v][0];
-                    y[v][1] = rotated<4>(x[v][0]);
-                    y[v][2] = rotated<8>(x[v][0]);
-                    y[v][3] = rotated<12>(x[v][0]);
+                    const u32x4 z = kShared && v == 1 ? rotated<2>(x[0][0]) : x[v % kPlanes][0];
+                    y[v][0] = z;
+                    y[v][1] = rotated<4>(z);
+                    y[v][2] = rotated<8>(z);
+                    y[v][3] = rotated<12>(z);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        y[v][c] = x[v][c % kXLoads];
+                        y[v][c] = x[v % kPlanes][c % kXLoads];
                 }
             }
 #pragma unroll
@@ -457,7 +465,7 @@ struct StepScales {
 template <class S>
 struct Kind {
     using type = S;
-    static constexpr bool kPacked = S::kPacked;
+    static constexpr int kColumns = S::kColumns;
 };
 
 // Gate and up, of 8 R hidden columns a block.
@@ -470,7 +478,8 @@ __global__ __launch_bounds__(kUpWaves * kWave) void block_few_up_kernel(FewArgs 
     static_assert(More::kBytes <= kRing && sizeof(f32x4) * R * kWave <= kRing, "LDS of a wave");
     constexpr int kCols = 8 * R;
     __shared__ __align__(1024) uint8_t s_ring[kUpWaves][kRing];
-    static_assert(sizeof s_ring >= kMaxWords * 4, "the routing's scratch");
+    static_assert(sizeof s_ring >= 16384 + kMaxWords * 4 && sizeof(Routing) <= 16384,
+                  "the routing lies in the rings, before they are used");
     __shared__ int s_list[kUpWaves][kFewMaxTokens];
     const uint32_t ring0 =
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&s_ring[0][0];
@@ -478,12 +487,15 @@ __global__ __launch_bounds__(kUpWaves * kWave) void block_few_up_kernel(FewArgs 
     const int wave = uniform(threadIdx.x / kWave);
     const int tiles = a.I / kCols;
     const int u = (int)blockIdx.x / tiles, tile = (int)blockIdx.x % tiles;
-    with_routing<kSmall, kUpWaves * kWave>(a, s_ring[0], [&](const auto& routing) {
+    uint8_t* mem = s_ring[0];
+    with_routing<kSmall, kUpWaves * kWave>(a, mem, mem + 16384, [&](const auto& routing) {
         if (u >= routing.hits)
             return;  // the whole block
         const int e = routing.expert(u);
         int* list = s_list[wave];  // every wave has its own
         const int n = routing.slots_of(a, e, list);
+        if (!kSmall)
+            __syncthreads();  // the routing has been read
         // operands: R / 2 of gate rows, then the same of up rows
         const int64_t row = (int64_t)e * 2 * a.I + tile * kCols;
         const uint8_t* rows[R];
@@ -503,7 +515,7 @@ __global__ __launch_bounds__(kUpWaves * kWave) void block_few_up_kernel(FewArgs 
         for (int c0 = 0; c0 < n; c0 += 16) {
             auto sums = [&](auto kind) {
                 using S = decltype(kind);
-                const int c = c0 + (lane & (S::kPacked ? 3 : 15));
+                const int c = c0 + (lane & (S::kColumns - 1));
                 const uint32_t column =
                     c < n ? (uint32_t)(list[c] / a.topk) * (uint32_t)a.H * 2u : kNowhere;
                 f32x4 acc[R];
@@ -579,10 +591,13 @@ __global__ __launch_bounds__(kDownWaves * kWave) void block_few_down_kernel(FewA
     using Few = Sums<R, 4, 2, WT, 0, D>;
     using More = Sums<R, 16, 2, WT, 0, 1>;
     constexpr int kRing = D * Few::kBytes > More::kBytes ? D * Few::kBytes : More::kBytes;
+    using Two = Sums<R, 2, 2, WT, 0, kRing / Sums<R, 2, 2, WT, 0, 1>::kBytes>;  // as many as fit
     extern __shared__ __align__(1024) uint8_t s_mem[];  // rings, [splits][T * topk][16 R] sums
     __shared__ int s_list[kDownWaves][kFewMaxTokens];
-    __shared__ int s_id[kSmall ? kWave : 1];
-    const int* id = s_id;  // the experts of the slots that are their token's first of it
+    // the routing, or (kSmall) the experts of the slots that are their token's first of it
+    __shared__ int s_routing[kSmall ? kWave : (sizeof(Routing) + 3) / 4];
+    const int* id = s_routing;
+    static_assert(offsetof(Routing, id) == 0, "the experts of the slots come first");
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
     uint8_t* ring = s_mem + wave * kRing;
@@ -592,12 +607,10 @@ __global__ __launch_bounds__(kDownWaves * kWave) void block_few_down_kernel(FewA
     constexpr int kCols = 16 * R;
     const int h0 = (int)blockIdx.x * kCols;
     const int P = a.T * a.topk;
-    with_routing<kSmall, kDownWaves * kWave>(a, s_mem, [&](const auto& routing) {
+    with_routing<kSmall, kDownWaves * kWave>(a, s_routing, s_mem, [&](const auto& routing) {
         if constexpr (kSmall) {
             if (wave == 0)
-                s_id[lane] = routing.id;
-        } else {
-            id = routing.s.id;
+                s_routing[lane] = routing.id;
         }
         const int steps = (a.I + kBlockK - 1) / kBlockK;
         const int items = routing.hits * a.splits;
@@ -620,7 +633,7 @@ __global__ __launch_bounds__(kDownWaves * kWave) void block_few_down_kernel(FewA
             for (int c0 = 0; c0 < n; c0 += 16) {
                 auto sums = [&](auto kind) {
                     using S = decltype(kind);
-                    const int cx = c0 + (lane & (S::kPacked ? 3 : 15));
+                    const int cx = c0 + (lane & (S::kColumns - 1));
                     const uint32_t column = cx < n ? (uint32_t)list[cx] * (uint32_t)a.I * 2u : kNowhere;
                     f32x4 acc[R];
 #pragma unroll
@@ -638,7 +651,9 @@ __global__ __launch_bounds__(kDownWaves * kWave) void block_few_down_kernel(FewA
                             *reinterpret_cast<f32x4*>(y + r * 16) = acc[r];
                     }
                 };
-                if (n <= 4)
+                if (n <= 2)
+                    sums(Kind<Two>());
+                else if (n <= 4)
                     sums(Kind<Few>());
                 else
                     sums(Kind<More>());
@@ -686,7 +701,7 @@ hipError_t launch_down(const FewArgs& a, hipStream_t s)
     constexpr int kFew = Sums<R, 4, 2, WT, 0, D>::kBytes * D, kMore = Sums<R, 16, 2, WT, 0, 1>::kBytes;
     const size_t lds = (size_t)kDownWaves * (kFew > kMore ? kFew : kMore) +
                        (size_t)a.splits * a.T * a.topk * 16 * R * sizeof(float);
-    constexpr size_t kStatic = (kSmall ? kWave * sizeof(int) : sizeof(Routing) + sizeof(int)) +
+    constexpr size_t kStatic = (kSmall ? kWave * sizeof(int) : sizeof(Routing)) +
                                kDownWaves * kFewMaxTokens * sizeof(int);
     if (lds + (kStatic + 1023) / 1024 * 1024 > kFewLds)
         return hipErrorInvalidValue;
