@@ -14,7 +14,13 @@
 //   sum d1 y = sum gh q + r2 (sum d2 q - mean(d2 n2) r2 sum h q),
 //   q = gate * post_weight * y, d2 = go * pre_weight,
 // and one exchange of six sums a row serves both. What bounds it is HBM
-// bandwidth: the next row is on its way while a row is worked on.
+// bandwidth: the next row is on its way while a row is worked on, and the
+// weights stay in registers, as a load of them between two rows would wait for
+// all of the next row. Measured on MI355X: 8 x 2048 rows of 7168 bf16 310 us (1.41
+// GB, 4.5 TB/s; 488 with the weights loaded each row and the waves' sums read one
+// by one) and 7 us for the second kernel, 4 x 256 rows of 4096 fp16, half of them
+// there, 15 and 4 us. Rows of more than 8192 elements leave no registers for the
+// next row and are read twice, the second time from the caches.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

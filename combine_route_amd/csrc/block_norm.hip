@@ -7,7 +7,10 @@
 // the last store, through the two sums of squares and, of INT8 rows, the
 // largest magnitude. The bound is HBM bandwidth in large calls and load
 // latency in small ones, so a row is shared by more waves the fewer rows
-// there are.
+// there are. Measured on MI355X: 8 x 4096 rows of 7168 bf16 with a gate a rank
+// to INT8 rows 286 us for 1.64 GB (5.8 TB/s; a 2 GB copy reaches 4.95), 128 rows
+// to bf16 and FP8 rows 6 us. (Weights asked for together with the row instead
+// of where they are used: 6.0 -> 6.2 us there, and a third more registers.)
 //
 // Each mean of squares is summed the same way whatever the number of waves:
 // FP32 sums of chunks of 512 elements (8 elements a lane in order, then a
