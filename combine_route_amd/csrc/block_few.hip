@@ -22,16 +22,14 @@
 // of a lane are widened to two operands of 8 values of the tokens' type, which
 // is exact for E4M3 and int8 alike, so that x needs no rounding; both sides take
 // k in the same permuted order. An expert with few columns has them loaded
-// packed (kinds Few and Two below), so that a load brings more of the weights'
-// companions than zeros. FP8 weights: the sum of each 128 elements of k is scaled
+// packed, so that a load brings more of them than zeros. FP8 weights: the sum of each 128 elements of k is scaled
 // as it joins the FP32 sum.
 //
 // Measured on MI355X (weights streamed to LDS alone: 7.0 TB/s): experts of 2048 x
 // 7168 FP8, top-8, one token 38 us for gate and up (6.2 TB/s) and 24 for down (4.8
-// TB/s); 64 tokens over 256 experts 950 (6.9 TB/s) and 660 us (5.0 TB/s: one block a
-// CU by its LDS, and between two experts a wave's ring runs empty). 4 tokens, top-4,
-// 1024 x 4096 INT8: 24 and 20 us, of which starting, routing and the last sums are
-// the larger part. With weights loaded to registers as the operands lie, 64 bytes of
+// TB/s); 64 tokens over 256 experts 950 (6.9 TB/s) and 618 us (5.3 TB/s: one block a
+// CU by its LDS, 448 blocks for 256 CUs). 4 tokens, top-4, 1024 x 4096 INT8: 24 and
+// 16.5 us, of which starting, routing and the last sums are the larger part. With weights loaded to registers as the operands lie, 64 bytes of
 // 16 rows a load, one token took 52 and 36 us.
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -53,6 +51,8 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kUpWaves = 4;
 constexpr int kDownWaves = 8;
+constexpr int kItemSteps = kWave;             // of an item whose scales lie in LDS
+constexpr int kItemScales = 2 * kItemSteps * 4;  // bytes a wave: of two items
 constexpr int kMaxWords = kFewMaxExperts / 32;
 constexpr int kBlockK = 128;  // elements of k a step
 constexpr uint32_t kNowhere = 1u << 31;
@@ -281,19 +281,16 @@ __device__ __forceinline__ u32x4 rotated(const u32x4& v)
 // Up to 4 columns lie packed: lane 4 c + i of each 16 has what column i
 // multiplies with the step's operand c, one load a step instead of four, and a
 // rotation of the 16 lanes by 4 c puts it in place (columns 4 and up hold what
-// nobody reads). Up to 2 columns of two planes share the load: lane 4 c + 2 v
-// + i has plane v's.
+// nobody reads).
 template <int R, int C, int X, int WT, int XT, int D>
 struct Sums {
     static constexpr bool kPacked = C <= 4;
-    static constexpr bool kShared = C <= 2 && X == 2;
-    static constexpr int kColumns = kShared ? 2 : kPacked ? 4 : 16;  // in turn over the lanes
-    static constexpr int kPlanes = kShared ? 1 : X;  // loaded apart
-    static constexpr int kXLoads = kPacked ? 1 : 4;  // a step and plane of columns
-    static constexpr int kAll = 2 * R + kPlanes * kXLoads;
+    static constexpr int kColumns = kPacked ? 4 : 16;  // in turn over the lanes
+    static constexpr int kXLoads = kPacked ? 1 : 4;    // a step and plane of columns
+    static constexpr int kAll = 2 * R + X * kXLoads;
     static constexpr int kBytes = kAll * 1024;       // a step's
 
-    u32x4 rw[R], rx[kPlanes];  // resources: 16 rows of K bytes each; the planes of the columns
+    u32x4 rw[R], rx[X];  // resources: 16 rows of K bytes each; the planes of the columns
     uint32_t lds0;       // of the ring
     const uint8_t* lds;
     uint32_t woff[2];    // this lane's chunk of the first step, in either 8 rows
@@ -313,8 +310,8 @@ struct Sums {
         for (int r = 0; r < R; ++r)
             rw[r] = rsrc_words(rows[r], bytes[r]);
 #pragma unroll
-        for (int v = 0; v < kPlanes; ++v)
-            rx[v] = rsrc_words(columns + (int64_t)v * plane, (int)(plane * (X / kPlanes)));
+        for (int v = 0; v < X; ++v)
+            rx[v] = rsrc_words(columns + (int64_t)v * plane, (int)plane);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int row = half * 8 + (lane >> 3), chunk = (lane & 7) ^ key(row);
@@ -323,8 +320,7 @@ struct Sums {
         }
         const int c = kPacked ? (lane & 15) >> 2 : 0;
         const int at = c / 2 * 64 + (lane >> 4) * 16 + c % 2 * 8;
-        const uint32_t second = kShared && (lane & 2) ? plane : 0u;
-        xoff = column == kNowhere ? kNowhere : column + second + (uint32_t)at * 2u;
+        xoff = column == kNowhere ? kNowhere : column + (uint32_t)at * 2u;
         xleft = K - at;
     }
 
@@ -349,100 +345,116 @@ struct Sums {
             const int more = i / 2 * 64 + i % 2 * 8;  // elements (packed: 0)
             const uint32_t to = mine && at + more < xleft ? xoff + more * 2u : kNowhere;
 #pragma unroll
-            for (int v = 0; v < kPlanes; ++v)
+            for (int v = 0; v < X; ++v)
                 load_to_lds<false>(rx[v], dst + (2 * R + v * kXLoads + i) * 1024, to,
                                    (uint32_t)at * 2u);
         }
     }
 
-    // scale(r, k): operand r's scale of step k, of FP8 weights.
-    template <class Scale>
-    __device__ __forceinline__ void operator()(int k0, Scale&& scale,
-                                               f32x4 (&acc)[R]) const
+    // The sums of the step that lies at `from` in the ring, once its loads have
+    // come; refill: loads into the place when it has been read. scale(r):
+    // operand r's scale, of FP8 weights.
+    template <class Scale, class Refill>
+    static __device__ __forceinline__ void step(const uint8_t* from, Scale&& scale,
+                                                Refill&& refill, f32x4 (&acc)[R])
     {
         const int lane = threadIdx.x & (kWave - 1);
         const int q = lane >> 4, i16 = lane & 15;
         const uint32_t wat = (uint32_t)i16 * 128u + (uint32_t)((q ^ key(i16)) * 16);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kAll) : "memory");
+        // taken here, so that no branch comes between the products and their
+        // scaling: behind one, the compiler left out the wait states that a
+        // matrix instruction's result needs (element 3 of each was wrong)
+        float f[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            f[r] = WT == 0 ? scale(r) : 1.0f;
+        u32x4 w[R][2], x[X][kXLoads];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)  // of the step: chunks q, q + 4
+                w[r][half] = *reinterpret_cast<const u32x4*>(from + r * 2048 + (wat ^ half * 64));
+#pragma unroll
+        for (int v = 0; v < X; ++v)
+#pragma unroll
+            for (int i = 0; i < kXLoads; ++i)
+                x[v][i] = *reinterpret_cast<const u32x4*>(
+                    from + (2 * R + v * kXLoads + i) * 1024 + lane * 16);
+        // read before the place is loaded again
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        refill();
+        __builtin_amdgcn_sched_barrier(0);
+
+        f32x4 sum[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            sum[r] = WT == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[r];
+        u32x4 y[X][4];
+#pragma unroll
+        for (int v = 0; v < X; ++v) {
+            if constexpr (kPacked) {
+                y[v][0] = x[v][0];
+                y[v][1] = rotated<4>(x[v][0]);
+                y[v][2] = rotated<8>(x[v][0]);
+                y[v][3] = rotated<12>(x[v][0]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    y[v][c] = x[v][c % kXLoads];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const u32x4 o = widened8<WT, XT>(w[r][c >> 1][(c & 1) * 2],
+                                                 w[r][c >> 1][(c & 1) * 2 + 1]);
+#pragma unroll
+                for (int v = 0; v < X; ++v)
+                    sum[r] = product<XT>(o, y[v][c], sum[r]);
+            }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if constexpr (WT == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[r][i] = __builtin_fmaf(f[r], sum[r][i], acc[r][i]);
+            } else {
+                acc[r] = sum[r];
+            }
+        }
+    }
+
+    // After the last step: its products' wait states, which a loop's end is a
+    // branch before; kDrain: and every load here, as loads past the end may not
+    // write what comes next in LDS.
+    template <bool kDrain>
+    static __device__ __forceinline__ void done()
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        if (kDrain)
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_nop 15" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // Steps [k0, k1). scale(r, k): operand r's scale of step k, of FP8 weights.
+    template <class Scale>
+    __device__ __forceinline__ void operator()(int k0, Scale&& scale, f32x4 (&acc)[R]) const
+    {
 #pragma unroll
         for (int d = 0; d < D; ++d)
             load(k0 + d, d);
         int slot = 0;
         for (int k = k0; k < k1; ++k) {
-            // taken here, so that no branch comes between the products and their
-            // scaling: behind one, the compiler left out the wait states that a
-            // matrix instruction's result needs (element 3 of each was wrong)
-            float f[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                f[r] = WT == 0 ? scale(r, k) : 1.0f;
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * kAll) : "memory");
-            const uint8_t* from = lds + slot * kBytes;
-            u32x4 w[R][2], x[kPlanes][kXLoads];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int half = 0; half < 2; ++half)  // of the step: chunks q, q + 4
-                    w[r][half] = *reinterpret_cast<const u32x4*>(from + r * 2048 +
-                                                                 (wat ^ half * 64));
-#pragma unroll
-            for (int v = 0; v < kPlanes; ++v)
-#pragma unroll
-                for (int i = 0; i < kXLoads; ++i)
-                    x[v][i] = *reinterpret_cast<const u32x4*>(
-                        from + (2 * R + v * kXLoads + i) * 1024 + lane * 16);
-            // read before the slot is loaded again
-            __builtin_amdgcn_sched_barrier(0);
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-            load(k + D, slot);
-            __builtin_amdgcn_sched_barrier(0);
+            step(lds + slot * kBytes, [&](int r) { return scale(r, k); },
+                 [&] { load(k + D, slot); }, acc);
             slot = slot + 1 == D ? 0 : slot + 1;
-
-            f32x4 sum[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                sum[r] = WT == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[r];
-            u32x4 y[X][4];
-#pragma unroll
-            for (int v = 0; v < X; ++v) {
-                if constexpr (kPacked) {
-                    const u32x4 z = kShared && v == 1 ? rotated<2>(x[0][0]) : x[v % kPlanes][0];
-                    y[v][0] = z;
-                    y[v][1] = rotated<4>(z);
-                    y[v][2] = rotated<8>(z);
-                    y[v][3] = rotated<12>(z);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        y[v][c] = x[v % kPlanes][c % kXLoads];
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const u32x4 o = widened8<WT, XT>(w[r][c >> 1][(c & 1) * 2],
-                                                     w[r][c >> 1][(c & 1) * 2 + 1]);
-#pragma unroll
-                    for (int v = 0; v < X; ++v)
-                        sum[r] = product<XT>(o, y[v][c], sum[r]);
-                }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if constexpr (WT == 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[r][i] = __builtin_fmaf(f[r], sum[r][i], acc[r][i]);
-                } else {
-                    acc[r] = sum[r];
-                }
-            }
         }
-        // loads past the end may not write what comes next in LDS; and the last
-        // products' wait states, which the loop's end is a branch before
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
+        done<true>();
     }
 };
 
@@ -603,8 +615,8 @@ __global__ __launch_bounds__(kDownWaves * kWave) void block_few_down_kernel(FewA
     using Few = Sums<R, 4, 2, WT, 0, D>;
     using More = Sums<R, 16, 2, WT, 0, 1>;
     constexpr int kRing = D * Few::kBytes > More::kBytes ? D * Few::kBytes : More::kBytes;
-    using Two = Sums<R, 2, 2, WT, 0, kRing / Sums<R, 2, 2, WT, 0, 1>::kBytes>;  // as many as fit
-    extern __shared__ __align__(1024) uint8_t s_mem[];  // rings, [splits][T * topk][16 R] sums
+    // rings, scales of two items a wave, [splits][T * topk][16 R] sums
+    extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ int s_list[kDownWaves][kFewMaxTokens];
     // the routing, or (kSmall) the experts of the slots that are their token's first of it
     __shared__ int s_routing[kSmall ? kWave : (sizeof(Routing) + 3) / 4];
@@ -615,7 +627,10 @@ __global__ __launch_bounds__(kDownWaves * kWave) void block_few_down_kernel(FewA
     uint8_t* ring = s_mem + wave * kRing;
     const uint32_t ring0 =
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring;
-    float* s_y = reinterpret_cast<float*>(s_mem + kDownWaves * kRing);
+    float* s_scale = reinterpret_cast<float*>(s_mem + kDownWaves * kRing + wave * kItemScales);
+    const uint32_t scale0 =
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)s_scale;
+    float* s_y = reinterpret_cast<float*>(s_mem + kDownWaves * (kRing + kItemScales));
     constexpr int kCols = 16 * R;
     const int h0 = (int)blockIdx.x * kCols;
     const int P = a.T * a.topk;
@@ -627,49 +642,131 @@ __global__ __launch_bounds__(kDownWaves * kWave) void block_few_down_kernel(FewA
         const int steps = (a.I + kBlockK - 1) / kBlockK;
         const int items = routing.hits * a.splits;
         int* list = s_list[wave];
-        for (int item = wave; item < items; item += kDownWaves) {
-            const int e = routing.expert(item / a.splits), split = item % a.splits;
-            const int n = routing.slots_of(a, e, list);
-            const int k0 = uniform(steps * split / a.splits);
-            const int k1 = uniform(steps * (split + 1) / a.splits);
-            const int64_t row = (int64_t)e * a.H + h0;
+        // One piece of an expert's k: what its sums need.
+        struct Item {
+            int n, split, k0, k1;
             const uint8_t* rows[R];
             int bytes[R];
+            const float* scales;  // (a block's columns lie in one block of 128)
+        };
+        auto look_up = [&](int item) {
+            Item it;
+            const int e = routing.expert(item / a.splits);
+            it.split = item % a.splits;
+            it.n = routing.slots_of(a, e, list);
+            it.k0 = uniform(steps * it.split / a.splits);
+            it.k1 = uniform(steps * (it.split + 1) / a.splits);
+            const int64_t row = (int64_t)e * a.H + h0;
 #pragma unroll
             for (int r = 0; r < R; ++r) {  // (H may end inside the block)
-                rows[r] = a.down + (row + r * 16) * a.I;
-                bytes[r] = h0 + r * 16 < a.H ? a.I * 16 : 0;
+                it.rows[r] = a.down + (row + r * 16) * a.I;
+                it.bytes[r] = h0 + r * 16 < a.H ? a.I * 16 : 0;
             }
-            // (a block's columns lie in one block of 128)
-            const float* first = a.downs + (WT == 0 ? (row / 128) * (a.I / kBlockK) : 0);
-            for (int c0 = 0; c0 < n; c0 += 16) {
-                auto sums = [&](auto kind) {
-                    using S = decltype(kind);
-                    const int cx = c0 + (lane & (S::kColumns - 1));
-                    const uint32_t column = cx < n ? (uint32_t)list[cx] * (uint32_t)a.I * 2u : kNowhere;
-                    f32x4 acc[R];
+            it.scales = a.downs + (WT == 0 ? (row / 128) * (a.I / kBlockK) : 0);
+            return it;
+        };
+        const uint32_t plane = (uint32_t)P * (uint32_t)a.I * 2u;
+        auto column_of = [&](int slot) {
+            return slot < 0 ? kNowhere : (uint32_t)slot * (uint32_t)a.I * 2u;
+        };
+        // acc: 4 output columns a lane and operand of the pair `slot`
+        auto keep = [&](const f32x4 (&acc)[R], int split, int slot) {
+            float* y = s_y + (split * P + slot) * kCols + (lane >> 4) * 4;
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                    StepScales sc(first, k0, WT == 0 ? k1 : k0);
-                    typename S::type(rows, bytes, a.act, (uint32_t)P * (uint32_t)a.I * 2u, column,
-                                     a.I, k1, ring, ring0)(
-                        k0, [&](int, int k) { return sc.at(k); }, acc);
-                    const int c = c0 + (lane & 15);
-                    if (c < n) {
-                        float* y = s_y + (split * P + list[c]) * kCols + (lane >> 4) * 4;
+            for (int r = 0; r < R; ++r)
+                *reinterpret_cast<f32x4*>(y + r * 16) = acc[r];
+        };
+        // Experts of up to 4 columns, one after the other, keep the ring full:
+        // the next one's first steps are loaded in the last steps of one (64
+        // tokens over 256 experts, inter 2048: 662 us without, 618 so). So that a wave is
+        // at most one ahead, an item has D steps at least; its scales lie in LDS
+        // too, as a load to a register would wait for the ring's before it.
+        const bool chained =
+            steps / a.splits >= D && (steps + a.splits - 1) / a.splits <= kItemSteps;
+        int item = wave;  // the one that is loaded
+        while (item < items) {
+            Item it = look_up(item);
+            if (it.n > 4 || !chained) {
+                for (int c0 = 0; c0 < it.n; c0 += 16) {
+                    auto sums = [&](auto kind) {
+                        using S = decltype(kind);
+                        const int cx = c0 + (lane & (S::kColumns - 1));
+                        f32x4 acc[R];
 #pragma unroll
                         for (int r = 0; r < R; ++r)
-                            *reinterpret_cast<f32x4*>(y + r * 16) = acc[r];
-                    }
-                };
-                if (n <= 2)
-                    sums(Kind<Two>());
-                else if (n <= 4)
-                    sums(Kind<Few>());
-                else
-                    sums(Kind<More>());
+                            acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                        StepScales sc(it.scales, it.k0, WT == 0 ? it.k1 : it.k0);
+                        typename S::type(it.rows, it.bytes, a.act, plane,
+                                         column_of(cx < it.n ? list[cx] : -1), a.I, it.k1, ring,
+                                         ring0)(
+                            it.k0, [&](int, int k) { return sc.at(k); }, acc);
+                        const int c = c0 + (lane & 15);
+                        if (c < it.n)
+                            keep(acc, it.split, list[c]);
+                    };
+                    if (it.n <= 4)
+                        sums(Kind<Few>());
+                    else
+                        sums(Kind<More>());
+                }
+                item += kDownWaves;
+                continue;
             }
+            int half = 0;  // of s_scale, the loaded item's
+            // (lane & 15) < n: the pair of this lane's column
+            auto open = [&](const Item& at, int& slot) {
+                slot = (lane & 3) < at.n ? list[lane & 3] : -1;
+                if (WT == 0)
+                    load4_to_lds(rsrc_words(at.scales + at.k0, (at.k1 - at.k0) * 4),
+                                 scale0 + half * kItemSteps * 4, lane * 4u);
+                return Few(at.rows, at.bytes, a.act, plane, column_of(slot), a.I, at.k1, ring,
+                           ring0);
+            };
+            int slot, next_slot = -1;
+            Few from = open(it, slot);
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                from.load(it.k0 + d, d);
+            int loaded = it.k0 + D, place = 0;
+            for (;;) {
+                bool more = false;
+                Item next = it;
+                f32x4 acc[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                const float* scales = s_scale + half * kItemSteps;
+                for (int k = it.k0; k < it.k1; ++k) {
+                    Few::step(
+                        ring + place * Few::kBytes, [&](int) { return scales[k - it.k0]; },
+                        [&] {
+                            if (loaded == from.k1) {  // (past it: nothing is loaded any more)
+                                item += kDownWaves;
+                                if (item < items) {
+                                    next = look_up(item);
+                                    if (next.n <= 4) {
+                                        more = true;
+                                        half ^= 1;
+                                        from = open(next, next_slot);
+                                        loaded = next.k0;
+                                    }
+                                }
+                            }
+                            from.load(loaded, place);
+                            ++loaded;
+                        },
+                        acc);
+                    place = place + 1 == D ? 0 : place + 1;
+                }
+                Few::template done<false>();
+                if ((lane & 15) < it.n)
+                    keep(acc, it.split, slot);
+                if (!more)
+                    break;
+                it = next;
+                slot = next_slot;
+            }
+            Few::template done<true>();
         }
     });
     __syncthreads();
@@ -711,7 +808,7 @@ template <int WT, int XT, int R, int D, bool kSmall>
 hipError_t launch_down(const FewArgs& a, hipStream_t s)
 {
     constexpr int kFew = Sums<R, 4, 2, WT, 0, D>::kBytes * D, kMore = Sums<R, 16, 2, WT, 0, 1>::kBytes;
-    const size_t lds = (size_t)kDownWaves * (kFew > kMore ? kFew : kMore) +
+    const size_t lds = (size_t)kDownWaves * ((kFew > kMore ? kFew : kMore) + kItemScales) +
                        (size_t)a.splits * a.T * a.topk * 16 * R * sizeof(float);
     constexpr size_t kStatic = (kSmall ? kWave * sizeof(int) : sizeof(Routing)) +
                                kDownWaves * kFewMaxTokens * sizeof(int);
@@ -737,9 +834,11 @@ hipError_t few_with(const FewArgs& a, hipStream_t s)
     // the pairs' sums leave LDS for three steps; else 16, with two steps of the
     // largest calls
     const int pairs = a.splits * a.T * a.topk;
-    if (kSmall && a.H >= 32 * 192 && pairs <= 64)
-        return launch_down<WT, XT, 2, 3, kSmall>(a, s);
-    if (pairs <= 832)
+    if constexpr (kSmall) {
+        if (a.H >= 32 * 192 && pairs <= 64)
+            return launch_down<WT, XT, 2, 3, kSmall>(a, s);
+    }
+    if (pairs <= 768)
         return launch_down<WT, XT, 1, 3, kSmall>(a, s);
     return launch_down<WT, XT, 1, 2, kSmall>(a, s);
 }

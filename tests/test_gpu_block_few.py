@@ -80,6 +80,21 @@ def test_sizes_off_128(E, T, k, H, I, dtype):
     check(s, run(s))
 
 
+@pytest.mark.parametrize("E,T,k,H,I,kind", [
+    (100, 64, 8, 128, 384, "fp8"), (100, 64, 8, 128, 512, "int8"), (60, 30, 4, 256, 1024, "fp8"),
+    (60, 50, 8, 144, 400, "int8"), (40, 16, 3, 128, 2048, "int8"), (60, 8, 8, 6272, 640, "fp8"),
+    (80, 64, 16, 128, 640, "fp8")])
+def test_many_experts_of_few_and_many_columns(E, T, k, H, I, kind):
+    """Experts of 1 to 4 columns follow each other and ones of more, in a wave;
+    every eighth is named more often."""
+    s = make(E, T, k, H, I, BF16, kind, E + I)
+    g = torch.Generator().manual_seed(I)
+    score = torch.rand((T, E), generator=g) + 0.3 * (torch.arange(E) % 8 == 3)
+    s["ids"] = score.argsort(-1, descending=True)[:, :k].to(torch.int32).cuda()
+    for _ in range(2):
+        check(s, run(s))
+
+
 @pytest.mark.parametrize("kind", ["fp8", "int8"])
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("T", [1, 9, 40])
