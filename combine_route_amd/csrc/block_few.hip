@@ -3,13 +3,13 @@
 //
 // Such a call is its weights' bytes: 3 * inter * hidden for each expert hit,
 // against which tokens, hidden rows and arithmetic are nothing. So nothing is
-// gathered or packed, every weight byte is loaded once, and the two kernels
-// only see to it that enough loads are in flight: each wave has a ring in LDS
-// that its own loads fill ahead of it, 8 rows' whole cache lines a load, with
-// no barrier, as nobody else reads it.
+// gathered or packed, every weight byte is loaded once for each 16 tokens of
+// its expert, and the two kernels only see to it that enough loads are in
+// flight: each wave has a ring in LDS that its own loads fill ahead of it, 8
+// rows' whole cache lines a load, with no barrier, as nobody else reads it.
 //
-// The first kernel takes gate and up: a block has one expert and 8 or 16 hidden
-// columns, its 4 waves a quarter of k each; the quarters are added in order
+// The first kernel takes gate and up: a block has one expert and 16 or 32
+// hidden columns, its 4 waves a quarter of k each; the quarters are added in order
 // through LDS, and silu(gate) * up goes to the workspace as a bf16 value and
 // the bf16 value of its rest. The second takes down: a block has 16 or 32
 // output columns for every expert hit, its 8 waves share the experts (and pieces
@@ -22,15 +22,16 @@
 // of a lane are widened to two operands of 8 values of the tokens' type, which
 // is exact for E4M3 and int8 alike, so that x needs no rounding; both sides take
 // k in the same permuted order. An expert with few columns has them loaded
-// packed, so that a load brings more of them than zeros. FP8 weights: the sum of each 128 elements of k is scaled
-// as it joins the FP32 sum.
+// packed, so that a load brings more of them than zeros. FP8 weights: the sum
+// of each 128 elements of k is scaled as it joins the FP32 sum.
 //
 // Measured on MI355X (weights streamed to LDS alone: 7.0 TB/s): experts of 2048 x
 // 7168 FP8, top-8, one token 38 us for gate and up (6.2 TB/s) and 24 for down (4.8
 // TB/s); 64 tokens over 256 experts 950 (6.9 TB/s) and 618 us (5.3 TB/s: one block a
 // CU by its LDS, 448 blocks for 256 CUs). 4 tokens, top-4, 1024 x 4096 INT8: 24 and
-// 16.5 us, of which starting, routing and the last sums are the larger part. With weights loaded to registers as the operands lie, 64 bytes of
-// 16 rows a load, one token took 52 and 36 us.
+// 16.5 us, of which starting, routing and the last sums are the larger part. With
+// weights loaded to registers as the operands lie, 64 bytes of 16 rows a load, one
+// token took 52 and 36 us.
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
