@@ -247,7 +247,8 @@ def _prepare_norm(case, seed):
     s["workspace"] = None
     if own:  # which a training program keeps
         import combine_route_amd as cra
-        s["workspace"] = torch.empty(cra.moe_block_norm_backward_workspace_bytes(G * M, H, G),
+        groups = G if case["ragged"] or case["gate"] == "group" else 1
+        s["workspace"] = torch.empty(cra.moe_block_norm_backward_workspace_bytes(G * M, H, groups),
                                      dtype=torch.uint8, device="cuda")
     return s
 
