@@ -214,7 +214,8 @@ def moe_block_norm(y: torch.Tensor, residual: torch.Tensor, pre_weight: Optional
 
 def moe_block_norm_backward_workspace_bytes(rows: int, hidden: int, groups: int = 1) -> int:
     """Bytes of workspace that moe_block_norm_backward needs for rows of this
-    many groups (the gates of a gate [G, H], or the counts; else 1)."""
+    many groups (the gates of a gate [G, H], or the counts; else 1); enough for
+    calls on these rows in other groups, or none, too."""
     return _workspace_bytes("moe_block_norm_backward_workspace_bytes", rows, hidden, groups)
 
 

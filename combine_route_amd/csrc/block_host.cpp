@@ -95,9 +95,10 @@ int weight_type(int weight_dtype, int dtype)
 // Blocks of a grouped product: one a compute unit of an MI355X.
 constexpr int kGemmBlocks = 256;
 
-// How the backward's rows lie on its blocks.
+// How the backward's rows lie on its blocks. most_blocks: of these rows in any
+// number of groups.
 struct BackwardShape {
-    int chunks, row_waves, group_blocks, block_groups, blocks;
+    int chunks, row_waves, group_blocks, block_groups, blocks, most_blocks;
 };
 
 // Chunks a wave: as few as let 8 waves hold the row, at most 4 (then up to 16
@@ -112,6 +113,7 @@ bool backward_shape(int64_t rows, int hidden, int64_t groups, BackwardShape* s)
     s->chunks = chunks <= 8 ? 1 : chunks <= 16 ? 2 : 4;
     s->row_waves = (chunks + s->chunks - 1) / s->chunks;
     const int64_t target = 256 * std::max(1, 8 / s->row_waves);
+    s->most_blocks = (int)std::min(rows, target);
     if (groups >= target) {
         s->group_blocks = 1;
         const int64_t each = (groups + target - 1) / target;
@@ -228,7 +230,7 @@ size_t moe_block_norm_backward_workspace_bytes(int64_t rows, int32_t hidden, int
         return 0;
     }
     ok();
-    return (size_t)3 * s.blocks * hidden * sizeof(float);
+    return (size_t)3 * s.most_blocks * hidden * sizeof(float);
 }
 
 int moe_block_norm_backward(const moe_block_norm_backward_args_t* a, void* stream_ptr)

@@ -112,8 +112,10 @@ int moe_block_norm(const moe_block_norm_args_t *args, void *stream);
  *   workspace     moe_block_norm_backward_workspace_bytes(rows, hidden,
  *                 groups) bytes, groups = rows / gate_rows with a gate of
  *                 several rows, else rows / group_rows with row_counts, else
- *                 1 (with both, gate_rows has to be group_rows); may be NULL
- *                 if no gradient of a weight or gate is asked for.
+ *                 1 (with both, gate_rows has to be group_rows). What is
+ *                 enough for some number of groups is enough for any other
+ *                 of the same rows. May be NULL if no gradient of a weight or
+ *                 gate is asked for.
  *                 Overwritten; 16-byte aligned.
  * Rows past a count are neither read nor written and add nothing to the
  * sums; with rows == 0 (EP_OK) nothing is written. hidden and alignment as

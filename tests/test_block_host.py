@@ -248,6 +248,24 @@ def test_backward_workspace_bytes(fn):
             size(*bad)
 
 
+@pytest.mark.parametrize("hidden", [256, 1032, 4096, 7168, 16392])
+@pytest.mark.parametrize("rows", [1, 48, 768, 840, 1680, 15120])
+def test_a_backward_workspace_is_enough_for_any_groups(fn, hidden, rows):
+    """The size for some groups serves calls with others: those without counts
+    have one group, whatever their tensors' leading size."""
+    size = cra.moe_block_norm_backward_workspace_bytes
+    groups = [g for g in (1, 2, 3, 4, 5, 6, 7, 8, 24, 48, 105, 280, 840, 1680, 15120)
+              if rows % g == 0]
+    for g in groups:
+        a = block.MoeBlockNormBackwardArgs(**dict(
+            BACKWARD, rows=rows, hidden=hidden, row_counts=FAKE if g > 1 else None,
+            group_rows=rows // g, gate_rows=0, workspace_bytes=0))
+        assert fn("moe_block_norm_backward")(ctypes.byref(a), None) == cra.EP_ERR_SIZE
+        need = int(re.search(r"(\d+) are needed", cra.ep_last_error())[1])
+        assert need > 0
+        assert all(size(rows, hidden, other) >= need for other in groups)
+
+
 def test_tensors_off_the_gpu_are_refused():
     x = torch.zeros((2, 128), dtype=torch.bfloat16)
     w = torch.ones(128, dtype=torch.bfloat16)
