@@ -57,6 +57,7 @@ constexpr int kItemScales = 2 * kItemSteps * 4;  // bytes a wave: of two items
 constexpr int kMaxWords = kFewMaxExperts / 32;
 constexpr int kBlockK = 128;  // elements of k a step
 constexpr uint32_t kNowhere = 1u << 31;
+constexpr float kBf16Max = 0x1.FEp127f;
 constexpr size_t kFewLds = 160 * 1024;  // of a compute unit
 
 // 4 codes as 4 values of the tokens' type (XT 0 bf16, 1 fp16), exact. WT: 0
@@ -590,6 +591,13 @@ __global__ __launch_bounds__(kUpWaves * kWave) void block_few_up_kernel(FewArgs 
                     const float y = silu_times(g, up);
                     z[i] = round_to<0>(y);
                     rest[i] = z[i] == y ? 0.0f : y - z[i];  // (an infinity has no rest)
+                    if (__builtin_isinf(z[i]) && !__builtin_isinf(y)) {
+                        // a finite value past the largest of bf16: that and a rest,
+                        // held below what would make their sum 2^128
+                        z[i] = __builtin_copysignf(kBf16Max, y);
+                        rest[i] = __builtin_copysignf(
+                            __builtin_fminf(__builtin_fabsf(y - z[i]), kBf16Max * 0x1p-8f), y);
+                    }
                 }
                 const int64_t at = (int64_t)list[c] * a.I + col;
                 const int64_t plane = (int64_t)a.T * a.topk * a.I;

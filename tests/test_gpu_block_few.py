@@ -145,6 +145,36 @@ def test_values_that_are_no_numbers_stay_in_their_token():
 
 
 @pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T", [1, 7])
+def test_hidden_values_between_the_largest_of_bf16_and_of_binary32(kind, dtype, T):
+    """Finite hidden values that round to infinity in bf16: (2 - 2^-20) 2^127, the
+    gate 2^64 (silu gives it back), down a diagonal of 2^-100."""
+    n = 128
+    x = torch.zeros((T, n), dtype=dtype, device="cuda")
+    x[:, 0] = 1.0
+    sign = torch.tensor([(1.0, -1.0, 0.0)[i % 3] for i in range(n)])
+    up = torch.zeros((1, 2 * n, n))
+    up[0, :n, 0] = 1.0
+    up[0, n:, 0] = sign
+    s = dict(x=x, ids=torch.zeros((T, 1), dtype=torch.int32, device="cuda"), w=None)
+    one = (lambda t: t.to(torch.int8)) if kind == "int8" else (lambda t: t.to(E4M3))
+    s["up"], s["down"] = one(up).cuda(), one(torch.eye(n)[None]).cuda()
+    each = n if kind == "int8" else 1
+    s["ups"] = torch.cat((torch.full((1, each), 2.0 ** 64),
+                          torch.full((1, each), (2.0 - 2.0 ** -20) * 2.0 ** 63)), 1).cuda()
+    s["downs"] = torch.full((1, each), 2.0 ** -100).cuda()
+    if kind == "fp8":
+        s["ups"], s["downs"] = s["ups"][..., None].contiguous(), s["downs"][..., None].contiguous()
+    scale = 2.0 ** -15 if dtype == FP16 else 1.0  # 2^28 is no fp16 number
+    s["downs"] *= scale
+    out = run(s)
+    check(s, out)
+    want = (sign * 2.0 ** 28 * scale).to(dtype).cuda()
+    assert torch.equal(out, want.expand(T, n))
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
 @pytest.mark.parametrize("k", [2, 5, 8])
 def test_a_token_alone_is_the_token_in_a_batch(kind, k):
     s = make(10, 64, k, 384, 256, BF16, kind, 7)
