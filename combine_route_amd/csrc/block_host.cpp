@@ -151,6 +151,8 @@ int moe_block_norm(const moe_block_norm_args_t* a, void* stream_ptr)
     int rc = check_norm(a);
     if (rc != EP_OK)
         return rc;
+    if (a->rows == 0)  // before what is set: empty tensors have no address
+        return ok();
     if ((a->codes == nullptr) != (a->scales == nullptr))
         return fail(EP_ERR_ARG, "args.codes and args.scales must both be set or both NULL");
     if (a->codes && a->codes_dtype != EP_FP8_E4M3 && a->codes_dtype != MOE_INT8)
@@ -161,8 +163,6 @@ int moe_block_norm(const moe_block_norm_args_t* a, void* stream_ptr)
         return fail(EP_ERR_ARG, "args.hidden = %d: FP8 codes need a multiple of 128", a->hidden);
     if ((a->pre_weight == nullptr) != (!a->out && !a->codes))
         return fail(EP_ERR_ARG, "args.pre_weight must be set iff args.out or args.codes is");
-    if (a->rows == 0)
-        return ok();
     const Pointer ptrs[] = {{a->y, "args.y", kPtrAlign, true},
                             {a->residual, "args.residual", kPtrAlign, true},
                             {a->residual_out, "args.residual_out", kPtrAlign, true},
@@ -240,6 +240,8 @@ int moe_block_norm_backward(const moe_block_norm_backward_args_t* a, void* strea
     int rc = check_norm(a);
     if (rc != EP_OK)
         return rc;
+    if (a->rows == 0)
+        return ok();
     if ((a->pre_weight == nullptr) != (a->grad_out == nullptr))
         return fail(EP_ERR_ARG, "args.pre_weight and args.grad_out must both be set or both NULL");
     if (!a->grad_out && !a->grad_h)
@@ -250,8 +252,6 @@ int moe_block_norm_backward(const moe_block_norm_backward_args_t* a, void* strea
         return fail(EP_ERR_ARG, "args.grad_gate needs args.gate");
     if (a->grad_pre_weight && !a->pre_weight)
         return fail(EP_ERR_ARG, "args.grad_pre_weight needs args.pre_weight");
-    if (a->rows == 0)
-        return ok();
     const bool sums = a->grad_post_weight || a->grad_gate || a->grad_pre_weight;
     const Pointer ptrs[] = {{a->y, "args.y", kPtrAlign, true},
                             {a->h, "args.h", kPtrAlign, a->grad_out != nullptr},

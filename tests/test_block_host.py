@@ -235,6 +235,21 @@ def test_calls_without_rows_are_no_work(fn):
         assert fn(name)(None, None) == cra.EP_ERR_NULL
 
 
+def test_norms_without_rows_take_any_pointers(fn):
+    """Empty tensors have no address: which of them are given cannot be told."""
+    a = block.MoeBlockNormArgs(**dict(NORM, rows=0, y=None, residual=None, residual_out=None,
+                                      out=None, codes=None, scales=None))
+    assert fn("moe_block_norm")(ctypes.byref(a), None) == cra.EP_OK
+    a = block.MoeBlockNormArgs(**dict(NORM, rows=0, codes=None))
+    assert fn("moe_block_norm")(ctypes.byref(a), None) == cra.EP_OK
+    a = block.MoeBlockNormBackwardArgs(**dict(BACKWARD, rows=0, y=None, h=None, grad_h=None,
+                                              grad_out=None, grad_y=None, grad_residual=None))
+    assert fn("moe_block_norm_backward")(ctypes.byref(a), None) == cra.EP_OK
+    # sizes are still checked
+    a = block.MoeBlockNormArgs(**dict(NORM, rows=0, out=None, hidden=12))
+    assert fn("moe_block_norm")(ctypes.byref(a), None) == cra.EP_ERR_ARG
+
+
 def test_backward_workspace_bytes(fn):
     size = cra.moe_block_norm_backward_workspace_bytes
     assert size(64, 256, 4) == 64 * 256 * 12

@@ -166,6 +166,26 @@ def test_rows_without_numbers():
     assert torch.equal(o["scales"], torch.full_like(o["scales"], 2.0 ** -100 / 127))
 
 
+@pytest.mark.parametrize("shape", [(0, 128), (3, 0, 128), (0, 5, 128)])
+@pytest.mark.parametrize("quant", [None, "fp8", "int8"])
+def test_no_rows(shape, quant):
+    y = torch.empty(shape, dtype=BF16, device="cuda")
+    w = torch.ones(128, dtype=BF16, device="cuda")
+    codes = scales = None
+    if quant:
+        codes = torch.empty(shape, dtype=torch.int8 if quant == "int8" else E4M3, device="cuda")
+        scales = torch.empty(shape[:-1] + ((1,) if quant == "fp8" else ()), device="cuda")
+    for gate in (None, w, w.repeat(3, 1)) if shape[0] == 3 else (None, w):
+        cra.moe_block_norm(y, y, w, 1e-6, out=y, post_weight=w, gate=gate, codes=codes,
+                           scales=scales)
+        cra.moe_block_norm(y, y, None, 1e-6, post_weight=w, gate=gate)
+        cra.moe_block_norm_backward(y, y, 1e-6, y, grad_out=y, grad_h=y, grad_residual=y,
+                                    pre_weight=w, post_weight=w, gate=gate)
+    if quant == "int8":
+        cra.moe_quantize_int8(y, codes, scales)
+    torch.cuda.synchronize()
+
+
 def backward_inputs(G, M, H, dtype, wt, post, gate, pre, gh, seed):
     s = inputs(G, M, H, dtype, wt, post, gate, seed)
     s["h"] = s.pop("residual")
