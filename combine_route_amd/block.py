@@ -109,6 +109,16 @@ def _workspace_bytes(name, *sizes):
     return n
 
 
+def _torch_stream(stream, index):
+    """A call's stream as torch's object; None stays None (the current one)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    # (torch's ExternalStream takes handle 0, the default stream, for none)
+    handle, device = int(stream), torch.device("cuda", index)
+    return (torch.cuda.ExternalStream(handle, device=device) if handle
+            else torch.cuda.default_stream(device))
+
+
 def _workspace(given, nbytes, index, stream):
     """The given workspace, or a new one that torch's allocator owns on the
     call's stream."""
@@ -123,16 +133,8 @@ def _workspace(given, nbytes, index, stream):
         if have < nbytes:
             raise ValueError(f"workspace holds {have} bytes; this call needs {nbytes}")
         return given
-    device = torch.device("cuda", index)
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        # (torch's ExternalStream takes handle 0, the default stream, for none)
-        handle = int(stream)
-        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
-                  else torch.cuda.default_stream(device))
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_torch_stream(stream, index)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def _rows_of(t, name):
@@ -236,9 +238,9 @@ def moe_block_norm_backward(y: torch.Tensor, h: Optional[torch.Tensor], eps: flo
     of its two results, grad_out (of out, codes' rounding taken as the identity)
     and grad_h (of residual_out); either may be None. Writes grad_y and, each
     if given, grad_residual, and in float32 grad_post_weight [H], grad_gate (the
-    gate's shape) and grad_pre_weight [H]. workspace: any tensor of
-    moe_block_norm_backward_workspace_bytes bytes that no other call uses at
-    the same time; None makes a new one."""
+    gate's shape) and grad_pre_weight [H], which are zeros if y has no rows.
+    workspace: any tensor of moe_block_norm_backward_workspace_bytes bytes that
+    no other call uses at the same time; None makes a new one."""
     index, shape, H, rows, dtype = _rows_of(y, "y")
     _index_of(grad_y, "grad_y")
     same = (y.dtype,)
@@ -264,6 +266,11 @@ def moe_block_norm_backward(y: torch.Tensor, h: Optional[torch.Tensor], eps: flo
         None if ws is None else ws.data_ptr(), _ptr(counts, "counts", shape[:1], _I32, index),
         nbytes, rows, group, gate_rows, H, dtype, wt, residual_scale, eps)
     _call("moe_block_norm_backward", index, stream, a)
+    if rows == 0:  # the library writes nothing: these are sums over no rows
+        with torch.cuda.stream(_torch_stream(stream, index)):
+            for t in (grad_pre_weight, grad_post_weight, grad_gate):
+                if t is not None:
+                    t.zero_()
 
 
 def moe_quantize_int8(rows: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,

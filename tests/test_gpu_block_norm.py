@@ -312,6 +312,24 @@ def test_gradients_in_place_and_of_few():
     assert torch.equal(only, want["grad_gate"])
 
 
+@pytest.mark.parametrize("shape", [(0, 64), (3, 0, 64), (0, 5, 64)])
+def test_gradients_of_no_rows_are_zeros(shape):
+    """As those of rows that are all past their counts."""
+    y = torch.empty(shape, dtype=BF16, device="cuda")
+    w = torch.ones(64, dtype=BF16, device="cuda")
+    side = torch.cuda.Stream()
+    for gate in (w, w.repeat(3, 1)) if shape[0] == 3 else (w,):
+        for stream in (None, side, side.cuda_stream, 0):
+            grads = [torch.full(g.shape, 77.0, device="cuda") for g in (w, w, gate)]
+            torch.cuda.synchronize()
+            cra.moe_block_norm_backward(y, y, 1e-6, y, grad_out=y, grad_h=y, grad_residual=y,
+                                        pre_weight=w, post_weight=w, gate=gate,
+                                        grad_pre_weight=grads[0], grad_post_weight=grads[1],
+                                        grad_gate=grads[2], stream=stream)
+            torch.cuda.synchronize()
+            assert all(bool((g == 0).all()) for g in grads)
+
+
 def test_streams_and_graphs():
     """A side stream, and a graph of both calls replayed over new inputs with
     eager calls on another workspace in between."""
