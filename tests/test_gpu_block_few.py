@@ -80,6 +80,37 @@ def test_sizes_off_128(E, T, k, H, I, dtype):
     check(s, run(s))
 
 
+@pytest.mark.parametrize("E,T,k,I", [(3, 1, 2, 48), (8, 4, 4, 160), (20, 4, 8, 400)])
+@pytest.mark.parametrize("H", [6160, 7152, 6176])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_output_columns_that_end_inside_a_block(E, T, k, I, H, dtype):
+    """32 output columns a block, of which the last may have 16."""
+    s = make(E, T, k, H, I, dtype, "int8", E + H)
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("E", [300, 5000, 65536])
+@pytest.mark.parametrize("T,k", [(9, 3), (64, 3), (64, 16)])
+def test_many_experts(E, T, k):
+    """Of few slots and of many, to the last expert there can be."""
+    s = make(E, T, k, 16, 16, BF16, "int8", E + T)
+    s["ids"][T - 1, 0] = E - 1
+    s["ids"][0, k - 1] = E - 1
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("E,T,k,H,I", [
+    (1, 1, 1, 33280, 128), (2, 6, 1, 33280, 128), (8, 2, 8, 128, 8320), (8, 6, 8, 128, 8320),
+    (8, 1, 8, 256, 16512)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+def test_more_steps_than_scales_are_held(E, T, k, H, I, dtype, kind):
+    """Over 64 steps of k a wave, in gate and up and in down, of few columns and
+    of many: FP8 scales are fetched again on the way."""
+    s = make(E, T, k, H, I, dtype, kind, T + H)
+    check(s, run(s))
+
+
 @pytest.mark.parametrize("E,T,k,H,I,kind", [
     (100, 64, 8, 128, 384, "fp8"), (100, 64, 8, 128, 512, "int8"), (60, 30, 4, 256, 1024, "fp8"),
     (60, 50, 8, 144, 400, "int8"), (40, 16, 3, 128, 2048, "int8"), (60, 8, 8, 6272, 640, "fp8"),

@@ -137,6 +137,24 @@ def test_without_counts_many_groups_and_tiles():
     check_rows(case, run_rows(case, n, FP16), n)
 
 
+@pytest.mark.parametrize("counted", [False, True])
+def test_more_groups_than_counts_are_held(counted):
+    """Past 1024 groups the counts come from memory between tiles: of small
+    groups, and of groups of several tiles and of every class."""
+    for G, cap, n, k in ((1500, 5, 272, 64), (1100, 330, 272, 272)):
+        case = product_case(G, cap, n, k, G)
+        m = [(37 * g * g + g) % (cap + 9) - 4 for g in range(G)] if counted else None
+        want = [max(0, min(cap, v)) for v in m] if counted else [cap] * G
+        check_rows(case, run_rows(case, m, BF16), want)
+        case = (case[0], case[1] * 8 / k ** 0.5, case[2], case[3])
+        out = torch.full((G, cap, n // 2), 77.0, dtype=BF16, device="cuda")
+        cra.moe_grouped_gemm_int8_swiglu(*case, out, counts=counts_of(m))
+        for g in [0, 1, 1023, 1024, 1025, G - 2, G - 1, *range(2, G, 61)]:
+            z, err = swiglu_reference(case, want[g], g)
+            close_to(out[g, :want[g]], z, BF16, 0.0, err)
+            assert bool((out[g, want[g]:] == 77).all())
+
+
 @pytest.mark.parametrize("G,cap,n,k,rows", [
     (8, 1100, 7168, 2048, [1100, 1000, 300, 64, 1024, 600, 700, 900]),
     (6, 800, 7168, 1024, [200, 190, 800, 130, 256, 769]),

@@ -312,6 +312,27 @@ def test_gradients_in_place_and_of_few():
     assert torch.equal(only, want["grad_gate"])
 
 
+@pytest.mark.parametrize("H", [1024, 8192, 8200, 16392, 32768])
+@pytest.mark.parametrize("rows", [3, 600])
+def test_gradients_in_place_of_rows_of_any_size(H, rows):
+    """Long rows are read twice, the second time between the stores to the same
+    buffers; 600 are several a block."""
+    s = backward_inputs(1, rows, H, BF16, BF16, True, "channel", True, True, H)
+    want = backward(s)
+    for y_of, res_of in (("y", "h"), ("gh", "go"), ("y", "go"), ("gh", "h")):
+        b = {k: s[k].clone() for k in ("y", "h", "gh", "go")}
+        o = {k: torch.full((H,), 5.0, device="cuda") for k in ("pre", "post", "gate")}
+        cra.moe_block_norm_backward(
+            b["y"], b["h"], 1e-6, b[y_of], grad_out=b["go"], grad_h=b["gh"],
+            grad_residual=b[res_of], pre_weight=s["pre"], post_weight=s["post"], gate=s["gate"],
+            residual_scale=0.7, grad_pre_weight=o["pre"], grad_post_weight=o["post"],
+            grad_gate=o["gate"])
+        assert torch.equal(b[y_of], want["grad_y"]) and torch.equal(b[res_of],
+                                                                    want["grad_residual"])
+        for k in o:
+            assert torch.equal(o[k], want["grad_" + k]), k
+
+
 @pytest.mark.parametrize("shape", [(0, 64), (3, 0, 64), (0, 5, 64)])
 def test_gradients_of_no_rows_are_zeros(shape):
     """As those of rows that are all past their counts."""
