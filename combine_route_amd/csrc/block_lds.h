@@ -71,13 +71,5 @@ __device__ __forceinline__ u32x4 rsrc_words(const void* base, int bytes)
                  (uint32_t)ep::dev::kRsrcWord3};
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, int64_t bytes)
-{
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    const uint64_t lo = (uint32_t)uniform((int)(uint32_t)p);
-    const uint64_t hi = (uint32_t)uniform((int)(uint32_t)(p >> 32));
-    return row_rsrc(reinterpret_cast<const void*>(lo | hi << 32), (uint32_t)uniform((int)bytes));
-}
-
 }  // namespace dev
 }  // namespace block
