@@ -59,29 +59,6 @@ __device__ __forceinline__ uint32_t int8x4(float f0, float f1, float f2, float f
     return code(f0) | code(f1) << 8 | code(f2) << 16 | code(f3) << 24;
 }
 
-// exp(-g) to 4 half steps (2 of v_exp_f32, a rounding of each factor) wherever it
-// is normal: 2 to the power of -g log2(e), which one float holds only to |g| half
-// steps of the result, as t + r, and 2^(t + r) = 2^t (1 + r ln 2). r is no number
-// or anything where t is infinite or 2^t is 0 or infinite: held to [-1, 1] (a NaN
-// to -1), it changes neither.
-__device__ __forceinline__ float exp_minus(float g)
-{
-    constexpr double kLog2e = 1.4426950408889634;
-    constexpr float hi = (float)kLog2e, lo = (float)(kLog2e - (double)hi);
-    const float t = -g * hi;
-    const float r = __builtin_fmaf(-g, lo, __builtin_fmaf(-g, hi, -t));
-    return __builtin_amdgcn_exp2f(t) *
-           __builtin_fmaf(__builtin_amdgcn_fmed3f(r, -1.0f, 1.0f), 0.6931471805599453f, 1.0f);
-}
-
-// silu(g) * u. Both sides of the quotient over 16, so that the reciprocal stays
-// in the normal range wherever the exponential is finite.
-__device__ __forceinline__ float silu_times(float g, float u)
-{
-    const float d = __builtin_fmaf(exp_minus(g), 0.0625f, 0.0625f);
-    return g * 0.0625f * __builtin_amdgcn_rcpf(d) * u;
-}
-
 // 8 weights as they lie. WT: 0 bf16, 1 fp16, 2 fp32.
 template <int WT>
 struct Weights8 {

@@ -8,54 +8,14 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
 
 #include "block_kernels.h"
-#include "ep_static.h"
+#include "moe_check.h"
 
 namespace {
 
-constexpr size_t kPtrAlign = 16;
-// Bytes a call may move before its rows stream past the caches: the 256 MB
-// last-level cache of an MI355X.
-constexpr int64_t kKeepBytes = 256ll << 20;
-
-int fail(int code, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    return ep::set_error(code, buf);
-}
-
-int ok() { return ep::set_error(EP_OK, ""); }
-
-struct Pointer {
-    const void* ptr;
-    const char* name;
-    size_t align;
-    bool required;
-};
-
-template <int N>
-int check_pointers(const Pointer (&p)[N])
-{
-    for (int i = 0; i < N; ++i) {
-        if (!p[i].ptr) {
-            if (p[i].required)
-                return fail(EP_ERR_NULL, "%s is NULL", p[i].name);
-            continue;
-        }
-        if (reinterpret_cast<uintptr_t>(p[i].ptr) % p[i].align)
-            return fail(EP_ERR_ALIGN, "%s = %p is not %zu-byte aligned", p[i].name, p[i].ptr,
-                        p[i].align);
-    }
-    return EP_OK;
-}
+using namespace moe::host;
 
 // Checks that the two norm calls share.
 template <class A>
@@ -91,9 +51,6 @@ int weight_type(int weight_dtype, int dtype)
 {
     return weight_dtype == MOE_FP32 ? 2 : dtype == EP_BF16 ? 0 : 1;
 }
-
-// Blocks of a grouped product: one a compute unit of an MI355X.
-constexpr int kGemmBlocks = 256;
 
 // How the backward's rows lie on its blocks. most_blocks: of these rows in any
 // number of groups.

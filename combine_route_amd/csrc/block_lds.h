@@ -1,57 +1,15 @@
-// Loads from memory straight to LDS, and the waits between them and the reads,
-// for the kernels that feed the matrix units from LDS.
+// Loads from memory straight to LDS for the kernels that feed the matrix units
+// from LDS: as moe_lds.h's, of 4 bytes.
 #pragma once
 
 #include "block_device.h"
+#include "moe_lds.h"
 
 namespace block {
 namespace dev {
 
-// The end of a phase: this wave's LDS reads have returned and at most N of its
-// loads are in flight; then the same holds for every wave.
-template <int N>
-__device__ __forceinline__ void phase_end()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-__device__ __forceinline__ void phase_end()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// 16 bytes a lane straight to LDS: lane i's to dst + 16 * i. NT: stream. In
-// assembly because the compiler makes every LDS read after the builtin wait
-// for all loads in flight (it cannot tell which slice a read is of); written
-// so, the only waits are the kernel's own. No register is written, so nothing
-// the load does later can meet the compiler's registers, and its own counted
-// waits only get stricter by loads it does not know of. M0 holds dst, an LDS
-// address, and is named as overwritten (the compiler warns that it would not
-// hand it out either). What is checked against the resource's bytes is off +
-// soff.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-template <bool NT>
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off, uint32_t soff)
-{
-    if constexpr (NT)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
-                     ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
-                     : "memory", "m0");
-    else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                     ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
-                     : "memory", "m0");
-}
-
 // 4 bytes a lane: lane i's to dst + 4 * i.
 __device__ __forceinline__ void load4_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off)
 {
@@ -60,16 +18,6 @@ __device__ __forceinline__ void load4_to_lds(u32x4 rsrc, uint32_t dst, uint32_t 
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
-
-// A base that every lane holds alike, and a resource over `bytes` of it, in
-// scalar registers.
-__device__ __forceinline__ u32x4 rsrc_words(const void* base, int bytes)
-{
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    return u32x4{(uint32_t)uniform((int)(uint32_t)p),
-                 (uint32_t)uniform((int)(uint32_t)(p >> 32)) & 0xFFFFu, (uint32_t)uniform(bytes),
-                 (uint32_t)ep::dev::kRsrcWord3};
-}
 
 }  // namespace dev
 }  // namespace block

@@ -73,7 +73,7 @@
 
 #include <type_traits>
 
-#include "moe_device.h"
+#include "moe_lds.h"
 
 namespace moe {
 namespace {
@@ -123,55 +123,10 @@ constexpr int kLdsBytes = lds_bytes(7);
 static_assert(lds_bytes(4) <= kLdsBytes && lds_bytes(2) <= kLdsBytes && lds_bytes(1) <= kLdsBytes,
               "LDS of a block");
 
-// The end of a phase: this wave's LDS reads have returned and at most N of its
-// loads are in flight; then the same holds for every wave.
-template <int N>
-__device__ __forceinline__ void phase_end()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-__device__ __forceinline__ void phase_end()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// 16 bytes a lane straight to LDS: lane i's to dst + 16 * i. NT: stream. In
-// assembly because the compiler makes every LDS read after the builtin wait
-// for all loads in flight (it cannot tell which slice a read is of); written
-// so, the only waits are this file's own. No register is written, so nothing
-// the load does later can meet the compiler's registers, and its own counted
-// waits only get stricter by loads it does not know of.
-// dst is an LDS address. M0 holds it, and is named as overwritten: the
-// compiler keeps no value of its own there across the statement (it warns that
-// it would not hand the register out either). What is checked against the resource's
-// bytes is off + soff, whichever part of it is past them (measured on gfx950,
-// soff past them too).
+// As load_to_lds, for those of lanes 0 to 31 that are active; the mask is as
+// before afterwards.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-template <bool NT>
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off, uint32_t soff)
-{
-    if constexpr (NT)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
-                     ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
-                     : "memory", "m0");
-    else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                     ::"s"(dst), "v"(off), "s"(rsrc), "s"(soff)
-                     : "memory", "m0");
-}
-
-// The same for those of lanes 0 to 31 that are active; the mask is as before
-// afterwards.
 __device__ __forceinline__ void load_half_to_lds(u32x4 rsrc, uint32_t dst, uint32_t off,
                                                  uint32_t soff)
 {
@@ -205,14 +160,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(u32x4 w)
 {
     const uint32_t lo = w[0], hi = w[1];
     return row_rsrc(reinterpret_cast<const void*>(lo | (uint64_t)hi << 32), w[2]);
-}
-
-__device__ __forceinline__ u32x4 rsrc_words(const uint8_t* base, int bytes)
-{
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    return u32x4{(uint32_t)uniform((int)(uint32_t)p),
-                 (uint32_t)uniform((int)(uint32_t)(p >> 32)) & 0xFFFFu, (uint32_t)uniform(bytes),
-                 (uint32_t)kRsrcWord3};
 }
 
 __device__ __forceinline__ i32x8 operand(const uint8_t* lo, const uint8_t* hi)
@@ -594,21 +541,6 @@ __device__ __forceinline__ void multiply(const Loads<TS, kSwiglu>& ld,
     phase_end();
 }
 
-// exp(-g) to 4 half steps (2 of v_exp_f32, a rounding of each factor) wherever it
-// is normal: 2 to the power of -g log2(e), which one float holds only to |g| half
-// steps of the result, as t + r, and 2^(t + r) = 2^t (1 + r ln 2). r is no number
-// or anything where t is infinite or 2^t is 0 or infinite: held to [-1, 1] (a NaN
-// to -1), it changes neither.
-__device__ __forceinline__ float exp_minus(float g)
-{
-    constexpr double kLog2e = 1.4426950408889634;
-    constexpr float hi = (float)kLog2e, lo = (float)(kLog2e - (double)hi);
-    const float t = -g * hi;
-    const float r = __builtin_fmaf(-g, lo, __builtin_fmaf(-g, hi, -t));
-    return __builtin_amdgcn_exp2f(t) *
-           __builtin_fmaf(__builtin_amdgcn_fmed3f(r, -1.0f, 1.0f), 0.6931471805599453f, 1.0f);
-}
-
 // The tile's sums to memory.
 template <int TS, int DT, bool kSwiglu>
 __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (*s_amax)[tile_rows(TS)],
@@ -656,11 +588,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t, float (
             for (int s = 0; s < kGate; ++s) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float g = acc[j][s][r];
-                    // both sides of the quotient over 16, so that the reciprocal
-                    // stays in the normal range wherever the exponential is finite
-                    const float d = __builtin_fmaf(exp_minus(g), 0.0625f, 0.0625f);
-                    const float z = g * 0.0625f * __builtin_amdgcn_rcpf(d) * acc[j][kGate + s][r];
+                    const float z = silu_times(acc[j][s][r], acc[j][kGate + s][r]);
                     acc[j][s][r] = z;
                     amax = __builtin_fmaxf(amax, __builtin_fabsf(z));
                 }
