@@ -20,7 +20,10 @@
 // GB, 4.5 TB/s; 488 with the weights loaded each row and the waves' sums read one
 // by one) and 7 us for the second kernel, 4 x 256 rows of 4096 fp16, half of them
 // there, 15 and 4 us. Rows of more than 8192 elements leave no registers for the
-// next row and are read twice, the second time from the caches.
+// next row and are read twice, the second time from the caches; their 96 sums a
+// lane do not fit the registers either (224 to 288 bytes a lane of scratch memory up
+// to 16384 elements, 776 to 964 above): 8192 rows of 16384 1116 us (1.4 TB/s), 4096
+// of 32768 1954 (0.8).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

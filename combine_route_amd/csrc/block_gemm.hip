@@ -30,8 +30,8 @@
 // ends up with runs of 8 consecutive columns of one token row.
 //
 // Measured on MI355X (a large INT8 library product 2.4 POP/s, FP8 2.8; weights
-// streamed to LDS alone 7.0 TB/s): 32 experts, 32768 rows, n 7168, k 2048 500 to 590
-// us (1.6 to 1.9 POP/s), gate and up, n 4096, k 7168 870 to 940 us (2.0 to 2.2); 256
+// streamed to LDS alone 7.0 TB/s): 32 experts, 32768 rows, n 7168, k 2048 500 to 600
+// us (1.6 to 1.9 POP/s), gate and up, n 4096, k 7168 870 to 960 us (2.0 to 2.2); 256
 // experts x 32 rows, n 7168, k 2048 717 us (5.4 TB/s), gate and up of 32 experts x
 // 32 rows 144 us (6.5 TB/s). Large tiles: matrix units busy 46 to 61% of the cycles,
 // at 1.8 GHz under this load. Without its loads gate and up takes 780 us, without
@@ -40,7 +40,8 @@
 // step's barrier. 256 x 32 rows without the stores: 580 us; 117 MB of scattered rows
 // in a stream of reads cost the rest, whatever their cache policy (through the L2,
 // streamed) and whether a store writes 32 bytes a row or whole lines (turned round
-// in LDS first).
+// in LDS first). Fewer tiles than compute units leave the rest idle: 8 experts x 256
+// rows, n 2048, k 7168 68 us (0.9 POP/s), 27 x 4 rows, n 256, k 4608 27 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

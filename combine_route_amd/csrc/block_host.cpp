@@ -59,8 +59,9 @@ struct BackwardShape {
 };
 
 // Chunks a wave: as few as let 8 waves hold the row, at most 4 (then up to 16
-// waves). Blocks: one a compute unit for rows of 5 waves and more, whose
-// sums take the registers of most of a unit; more of shorter rows.
+// waves). Blocks: one a compute unit for rows of 5 waves and more: 8 waves of
+// 2 chunks fill a unit (216 to 238 registers a lane), and of 1 chunk all but fill
+// it (127 to 138, where two blocks a unit would need 128); more of shorter rows.
 bool backward_shape(int64_t rows, int hidden, int64_t groups, BackwardShape* s)
 {
     if (rows < 1 || groups < 1 || groups > rows || rows % groups || hidden < 8 || hidden % 8 ||
