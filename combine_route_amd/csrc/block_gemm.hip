@@ -33,7 +33,7 @@
 // streamed to LDS alone 7.0 TB/s): 32 experts, 32768 rows, n 7168, k 2048 500 to 600
 // us (1.6 to 1.9 POP/s), gate and up, n 4096, k 7168 870 to 960 us (2.0 to 2.2); 256
 // experts x 32 rows, n 7168, k 2048 717 us (5.4 TB/s), gate and up of 32 experts x
-// 32 rows 144 us (6.5 TB/s). Large tiles: matrix units busy 46 to 61% of the cycles,
+// 32 rows 144 us (6.5 TB/s). Large tiles: matrix units busy 45 to 63% of the cycles,
 // at 1.8 GHz under this load. Without its loads gate and up takes 780 us, without
 // its stores 910, without its reads of LDS as long as with them: what bounds it is
 // the loads, whose requests fill the load path for half of each step, and the
