@@ -206,6 +206,21 @@ def test_hidden_values_between_the_largest_of_bf16_and_of_binary32(kind, dtype, 
 
 
 @pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("dtype,scale", [(FP16, 2.0 ** -20), (BF16, 2.0 ** -128)])
+@pytest.mark.parametrize("T", [1, 9])
+def test_values_below_the_normal_range_count(kind, dtype, scale, T):
+    """Rows of x that lie below the type's normal range are not taken for zero."""
+    s = make(4, T, 2, 256, 128, dtype, kind, 11)
+    s["x"].mul_(scale)
+    assert bool((s["x"] != 0).any()) and float(s["x"].abs().max()) < torch.finfo(dtype).tiny
+    s["ups"] /= scale if dtype == FP16 else 2.0 ** -100
+    s["downs"] /= 1.0 if dtype == FP16 else 2.0 ** -56
+    out = run(s)
+    check(s, out)
+    assert bool((out != 0).any())
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
 @pytest.mark.parametrize("k", [2, 5, 8])
 def test_a_token_alone_is_the_token_in_a_batch(kind, k):
     s = make(10, 64, k, 384, 256, BF16, kind, 7)

@@ -1,5 +1,6 @@
-"""The largest sizes that include/moe_block.h allows in each dimension, and calls
-from several threads on streams of their own at once."""
+"""The largest sizes that include/moe_block.h allows in each dimension, calls from
+several threads on streams of their own at once, and the INT8 experts on a stream
+of their own."""
 import threading
 
 import pytest
@@ -162,3 +163,33 @@ def test_two_threads_at_once():
     for v in threads:
         v.join()
     assert not failed, failed[:5]
+
+
+@pytest.mark.parametrize("cap", [7, 48])
+def test_int8_experts_on_a_stream(cap):
+    """All of dispatch, experts and combine on a side stream, with fewer places
+    than rows for some experts, is what it is on the current one."""
+    W, M, H, Er, K, inter = 2, 24, 256, 4, 2, 96
+    cfg = cra.make_config(W, H, M, Er, K, "fp8", "bf16", scale_dim=1)
+    x, s = codes((W, M, H), 1), rand((W, M, 1), 2, torch.float32).abs()
+    ids = torch.rand((W, M, W * Er), generator=gen(3), device="cuda").argsort(-1)[..., :K]
+    ids = ids.to(torch.int32).contiguous()
+    w = torch.rand((W, M, K), generator=gen(4), device="cuda")
+    up, down = codes((W * Er, 2 * inter, H), 5), codes((W * Er, H, inter), 6)
+    ups = rand((W * Er, 2 * inter), 7, torch.float32).abs() * 1e-3
+    downs = rand((W * Er, H), 8, torch.float32).abs() * 1e-3
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for stream in (None, side, side.cuda_stream):
+        op = cra.EpDispatchCombineOp(cfg, with_weights=False, expert_capacity=cap)
+        torch.cuda.synchronize()
+        px, count, _, _ = op.dispatch_standard_moe(x.view(torch.uint8), None, s, ids, stream=stream)
+        y = op.expert_mlp_int8(px, count, up, ups, down, downs, stream=stream)
+        out = op.combine_standard_moe(y, w, ids, stream=stream)
+        torch.cuda.synchronize()
+        got.append(out.clone())
+        assert cap > 7 or bool((count > cap).any())
+        op.close()
+    assert bool(got[0].isfinite().all()) and bool((got[0] != 0).any())
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
